@@ -173,6 +173,21 @@ flexq_status flexq_linear_static_scratch(const void* x_dev, int ldx, const void*
                                          const void* residual_dev, int ld_res, int epilogue,
                                          void* y_dev, int ldy, int force_splits, void* stream);
 
+/* flexq_linear for a few rows (1 <= m <= 16) and a 4-bit weight: the products
+ * of a step over one to sixteen sequences, where reading the weight once is the
+ * whole cost.  w_dev: the tiled layout of flexq_packed_weight_bytes, used with
+ * flexq_linear's arithmetic (w = fp16(fp32(code * scale) + min), fp32 sums) and
+ * flexq_linear's epilogue flags; the two differ only in the order of the sums.
+ * x_dev fp16 [m][ldx] (ldx >= k, ldx % 8 == 0), residual_dev fp16 [m][ld_res],
+ * y_dev fp16 [m][ldy], or fp32 with flag 8.  y may be residual (same
+ * pointer and stride).  m == 0 does nothing; m > 16 returns
+ * FLEXQ_ERR_UNSUPPORTED (flexq_linear takes it).  No workspace: the
+ * parts of a K axis that is shared out are joined inside the launch, in a fixed
+ * order, so results do not depend on timing. */
+flexq_status flexq_gemv_q4(const void* x_dev, int ldx, const void* w_dev, int m, int n, int k,
+                           const void* bias_dev, const void* residual_dev, int ld_res, int epilogue,
+                           void* y_dev, int ldy, void* stream);
+
 /* LayerNorm of rows [rows][h] (biased variance, fp32 statistics). */
 flexq_status flexq_layernorm(const void* x_dev, int ldx, const void* gamma_dev,
                              const void* beta_dev, void* y_dev, int ldy, int rows, int h,
@@ -275,6 +290,95 @@ flexq_status flexq_attention_prefill(const flexq_config* cfg, const void* qkv_de
 flexq_status flexq_attention_prefill_cache(const flexq_config* cfg, const flexq_kv* kv, const void* q_dev,
                                            int ldq, int b, int s, int pos0, void* out_dev, int ldo,
                                            void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged KV cache: sequences of different lengths that come and go.           */
+/* ------------------------------------------------------------------------ */
+/* The cache above holds b sequences of one length.  Here the slots live in
+ * pages of a pool, and a table names the pages of each sequence; a batch is
+ * ragged: sequence i brings row_start[i+1] - row_start[i] new tokens (none,
+ * one, or a chunk of its prompt).  kv_heads may be less than heads
+ * (heads % kv_heads == 0: query head j reads key/value head
+ * j / (heads / kv_heads)). */
+
+/* One layer's pool.  A page is a flexq_kv sequence of page_size slots with
+ * kv_heads heads: kv_bits 4: k codes [num_pages][kv_heads][page_size][d/2], v
+ * 32-bit words [num_pages][kv_heads][page_size/8][d] (nibble t of word
+ * (block, e) is token 8*block + t at dimension e), k_meta and v_meta (min, scale)
+ * fp16 pairs [num_pages][kv_heads][page_size][d/64]; kv_bits 16: k, v fp16
+ * [num_pages][kv_heads][page_size][d], metas NULL.  All 16-byte aligned.
+ * page_size: a power of two, 8 to 1024.  table_dev: int32 [b][table_ld]; token
+ * p of sequence i lives in page table[i][p / page_size], slot p % page_size.
+ * Sequences may share pages that are only read (a common prefix); a page that
+ * new tokens are written to must belong to one sequence of the batch. */
+typedef struct {
+  void *k, *v, *k_meta, *v_meta;
+  int kv_heads, num_pages, page_size;
+  const int32_t* table_dev;
+  int table_ld;
+} flexq_paged_kv;
+
+/* A ragged batch.  Rows row_start[i] .. row_start[i+1]-1 of the token buffers
+ * are the new tokens of sequence i, in order; kv_len[i] is its length with them
+ * (so its first new token has position kv_len[i] - n_i).  row_start_dev: int32
+ * [b+1], non-decreasing from row_start[0] >= 0; rows of the buffers outside
+ * row_start[0] .. row_start[b]-1 (padding of a captured batch) are neither read nor
+ * written.  Three bounds the host knows: rows (row_start[b] <= rows), max_new
+ * (n_i <= max_new; 1 selects the single-token form) and max_len (kv_len[i] <=
+ * max_len <= table_ld * page_size).  They may be loose: a captured graph is replayed
+ * with other lengths under the same bounds, at the cost of work planned for
+ * the bounds.  A sequence with n_i == 0 is skipped, its kv_len and table are
+ * not looked at.  A sequence that breaks a bound, a length below n_i, or a page
+ * id outside the pool is reported by flexq_device_status() (FLEXQ_ERR_DEVICE);
+ * nothing is read or written out of range, and what the call writes for that sequence
+ * is unspecified. */
+typedef struct {
+  int b;
+  int rows;
+  int max_new;
+  int max_len;
+  const int32_t* row_start_dev;
+  const int32_t* kv_len_dev;
+} flexq_ragged;
+
+/* Rotary positions: cos_sin_dev fp32 [max_pos][rot_dim], the cosines of the
+ * rot_dim/2 angles of a position, then their sines (16-byte aligned).  The first rot_dim
+ * (a multiple of 16, at most d) dimensions of a head are rotated in pairs:
+ * (e, e + rot_dim/2), or with interleaved (2e, 2e + 1): a' = a cos - b sin,
+ * b' = b cos + a sin, every operation rounded in fp32, the results to fp16. */
+typedef struct {
+  const float* cos_sin_dev;
+  int max_pos, rot_dim, interleaved;
+} flexq_rope;
+
+/* Bytes of one layer's pool: K + V + metadata (0 for bad arguments). */
+size_t flexq_paged_kv_bytes(const flexq_config* cfg, int kv_heads, int num_pages, int page_size);
+
+/* Appends the new tokens' keys and values: k_dev, v_dev fp16 [rows][ld] (head j
+ * at columns j*d ..), stored as flexq_kv_append stores them (the same codes).
+ * rope (NULL: none, as in OPT): the keys are rotated by their positions
+ * first, and with q_dev the queries (fp16 [rows][ldq], cfg->heads heads) are
+ * rotated into q_out_dev [rows][ldqo] (q_out may be q with the same stride); q_dev must be
+ * NULL without rope.  A position >= max_pos is a bad device-side input. */
+flexq_status flexq_paged_append(const flexq_config* cfg, const flexq_paged_kv* kv, const flexq_ragged* batch,
+                                const flexq_rope* rope, const void* k_dev, const void* v_dev, int ld,
+                                const void* q_dev, int ldq, void* q_out_dev, int ldqo, void* stream);
+
+/* The inverse for the same description: the cached keys and values of the last
+ * n_i tokens of every sequence as fp16 rows k_out_dev, v_out_dev [rows][ld]
+ * (4-bit: the dequantized codes).  n_i = kv_len[i] reads whole histories. */
+flexq_status flexq_paged_read(const flexq_config* cfg, const flexq_paged_kv* kv, const flexq_ragged* batch,
+                              void* k_out_dev, void* v_out_dev, int ld, void* stream);
+
+/* Attention of the new tokens over the paged cache, their own slots included
+ * (append first): the row at position p attends over positions 0..p,
+ * out[row][j*d ..] = softmax(q K^T / sqrt(d)) V with the cache's fp16
+ * values (4-bit: the dequantized codes).  q_dev fp16 [rows][ldq], out_dev fp16
+ * [rows][ldo].  Chunks of a prompt, single tokens, and both in one batch.  No
+ * workspace: the parts of a long history that is shared out are joined inside
+ * the launch, in a fixed order, so results do not depend on timing. */
+flexq_status flexq_attention_paged(const flexq_config* cfg, const flexq_paged_kv* kv, const flexq_ragged* batch,
+                                   const void* q_dev, int ldq, void* out_dev, int ldo, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Layer steps ([WT] "P/D阶段计算", pre-LN OPT block).                          */

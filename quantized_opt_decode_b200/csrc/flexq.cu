@@ -688,6 +688,171 @@ flexq_status flexq_attention_prefill_cache(const flexq_config* cfg, const flexq_
   return FLEXQ_OK;
 }
 
+// --- few-row product ------------------------------------------------------------
+flexq_status flexq_gemv_q4(const void* x_dev, int ldx, const void* w_dev, int m, int n, int k, const void* bias_dev,
+                           const void* residual_dev, int ld_res, int epilogue, void* y_dev, int ldy, void* stream) {
+  FQ_CHECK(m >= 0 && n > 0 && k > 0 && k % 64 == 0, "need m >= 0, n > 0 and k a positive multiple of 64");
+  FQ_CHECK(n <= (1 << 28) && k <= (1 << 20), "n above 2^28 or k above 2^20 is not supported");
+  FQ_CHECK(epilogue >= 0 && epilogue < 16, "unknown epilogue flags");
+  FQ_CHECK(!(epilogue & EPI_F32_OUT) || epilogue == EPI_F32_OUT, "fp32 output takes no other epilogue");
+  if (m > kGemvMaxRows)
+    return fail(FLEXQ_ERR_UNSUPPORTED, "m = %d: at most %d rows (flexq_linear takes more)", m, kGemvMaxRows);
+  if (m == 0) return FLEXQ_OK;
+  FQ_CHECK(x_dev && w_dev && y_dev, "NULL pointer");
+  FQ_CHECK(ldx >= k && ldx % 8 == 0 && aligned16(x_dev), "x needs ldx >= k, ldx %% 8 == 0, 16-byte alignment");
+  FQ_CHECK(aligned16(w_dev), "w must be 16-byte aligned");
+  FQ_CHECK(ldy >= n, "ldy must be >= n");
+  FQ_CHECK(!(epilogue & EPI_BIAS) || bias_dev, "bias flag without bias");
+  FQ_CHECK(!(epilogue & EPI_RESIDUAL) || (residual_dev && ld_res >= n), "residual flag without residual");
+  FQ_CHECK((reinterpret_cast<uintptr_t>(y_dev) & (epilogue & EPI_F32_OUT ? 3 : 1)) == 0 &&
+               (!(epilogue & EPI_BIAS) || (reinterpret_cast<uintptr_t>(bias_dev) & 1) == 0) &&
+               (!(epilogue & EPI_RESIDUAL) || (reinterpret_cast<uintptr_t>(residual_dev) & 1) == 0),
+           "y, bias and residual must be aligned to their elements");
+  FQ_CUDA(launch_gemv_q4(static_cast<const __half*>(x_dev), ldx, static_cast<const uint8_t*>(w_dev), m, n, k,
+                         static_cast<const __half*>(bias_dev), static_cast<const __half*>(residual_dev), ld_res,
+                         epilogue, y_dev, ldy, as_stream(stream)),
+          "gemv");
+  return FLEXQ_OK;
+}
+
+// --- paged cache ----------------------------------------------------------------
+namespace {
+
+constexpr int kMaxPagedLen = 1 << 24;   // positions of one sequence
+constexpr int kMaxPagedRows = 1 << 24;  // rows of a token buffer
+
+flexq_status check_kv_heads(const flexq_config* c, int kv_heads) {
+  FQ_CHECK(kv_heads > 0 && c->heads % kv_heads == 0, "kv_heads must be positive and divide heads (%d, got %d)",
+           c->heads, kv_heads);
+  return FLEXQ_OK;
+}
+
+flexq_status check_page_size(int page_size) {
+  FQ_CHECK(page_size >= 8 && page_size <= 1024 && (page_size & (page_size - 1)) == 0,
+           "page_size must be a power of two in 8..1024 (got %d)", page_size);
+  return FLEXQ_OK;
+}
+
+// Checks the cache and the batch of a paged call and fills their views.
+flexq_status check_paged(const flexq_config* c, const flexq_paged_kv* kv, const flexq_ragged* batch, PagedView* pv,
+                         RaggedView* rv) {
+  FQ_TRY(check_config(c));
+  FQ_CHECK(kv != nullptr, "paged cache is NULL");
+  FQ_TRY(check_kv_heads(c, kv->kv_heads));
+  FQ_TRY(check_page_size(kv->page_size));
+  FQ_CHECK(kv->num_pages > 0, "num_pages must be positive");
+  FQ_CHECK(kv->k && kv->v, "paged cache k / v is NULL");
+  FQ_CHECK(aligned16(kv->k) && aligned16(kv->v), "paged cache buffers must be 16-byte aligned");
+  FQ_CHECK(c->kv_bits == 16 || (kv->k_meta && kv->v_meta && aligned16(kv->k_meta) && aligned16(kv->v_meta)),
+           "a 4-bit paged cache needs k_meta and v_meta, 16-byte aligned");
+  FQ_CHECK(batch != nullptr, "batch is NULL");
+  FQ_CHECK(batch->b >= 0 && batch->rows >= 0, "b and rows must be >= 0");
+  FQ_CHECK(batch->b <= 65535 && batch->rows <= kMaxPagedRows, "b above 65535 or rows above 2^24 is not supported");
+  if (batch->b > 0 && batch->rows > 0) {
+    FQ_CHECK(kv->table_dev && (reinterpret_cast<uintptr_t>(kv->table_dev) & 3) == 0, "table is NULL or misaligned");
+    FQ_CHECK(batch->row_start_dev && batch->kv_len_dev && (reinterpret_cast<uintptr_t>(batch->row_start_dev) & 3) == 0 &&
+                 (reinterpret_cast<uintptr_t>(batch->kv_len_dev) & 3) == 0,
+             "row_start or kv_len is NULL or misaligned");
+    FQ_CHECK(batch->max_new >= 1, "max_new must be >= 1");
+    FQ_CHECK(batch->max_len >= 1 && batch->max_len <= kMaxPagedLen, "max_len must be in 1..2^24");
+    FQ_CHECK(kv->table_ld > 0 && static_cast<long long>(kv->table_ld) * kv->page_size >= batch->max_len,
+             "max_len %d exceeds a table row (%d pages of %d)", batch->max_len, kv->table_ld, kv->page_size);
+  }
+  pv->k = kv->k;
+  pv->v = kv->v;
+  pv->k_meta = kv->k_meta;
+  pv->v_meta = kv->v_meta;
+  pv->kv_heads = kv->kv_heads;
+  pv->num_pages = kv->num_pages;
+  pv->page_shift = 0;
+  while ((1 << pv->page_shift) < kv->page_size) ++pv->page_shift;
+  pv->table = kv->table_dev;
+  pv->table_ld = kv->table_ld;
+  rv->b = batch->b;
+  rv->rows = batch->rows;
+  rv->max_new = std::min(batch->max_new, std::max(batch->rows, 1));
+  rv->max_len = batch->max_len;
+  rv->row_start = batch->row_start_dev;
+  rv->kv_len = batch->kv_len_dev;
+  return FLEXQ_OK;
+}
+
+bool rows_ok(const void* p, int ld, int width) { return p && ld >= width && ld % 8 == 0 && aligned16(p); }
+
+}  // namespace
+
+size_t flexq_paged_kv_bytes(const flexq_config* cfg, int kv_heads, int num_pages, int page_size) {
+  if (check_config(cfg) != FLEXQ_OK || check_kv_heads(cfg, kv_heads) != FLEXQ_OK ||
+      check_page_size(page_size) != FLEXQ_OK || num_pages <= 0)
+    return 0;
+  const size_t elems = static_cast<size_t>(num_pages) * page_size * kv_heads * (cfg->h / cfg->heads);
+  return cfg->kv_bits == 16 ? 2 * elems * 2 : 2 * (elems / 2 + elems / 64 * 4);
+}
+
+flexq_status flexq_paged_append(const flexq_config* cfg, const flexq_paged_kv* kv, const flexq_ragged* batch,
+                                const flexq_rope* rope, const void* k_dev, const void* v_dev, int ld,
+                                const void* q_dev, int ldq, void* q_out_dev, int ldqo, void* stream) {
+  PagedView pv{};
+  RaggedView rv{};
+  FQ_TRY(check_paged(cfg, kv, batch, &pv, &rv));
+  const int d = cfg->h / cfg->heads;
+  RopeView rp{};
+  FQ_CHECK(rope != nullptr || q_dev == nullptr, "queries are only rotated: q without rope");
+  if (rope != nullptr) {
+    FQ_CHECK(rope->rot_dim >= 16 && rope->rot_dim % 16 == 0 && rope->rot_dim <= d,
+             "rot_dim must be a multiple of 16 in 16..%d (got %d)", d, rope->rot_dim);
+    FQ_CHECK(rope->max_pos > 0 && rope->cos_sin_dev && aligned16(rope->cos_sin_dev),
+             "rope needs max_pos > 0 and a 16-byte aligned table");
+    FQ_CHECK(rope->interleaved == 0 || rope->interleaved == 1, "interleaved must be 0 or 1");
+    rp.cos_sin = rope->cos_sin_dev;
+    rp.max_pos = rope->max_pos;
+    rp.rot_dim = rope->rot_dim;
+    rp.interleaved = rope->interleaved;
+  }
+  if (rv.b == 0 || rv.rows == 0) return FLEXQ_OK;
+  FQ_CHECK(rows_ok(k_dev, ld, pv.kv_heads * d) && rows_ok(v_dev, ld, pv.kv_heads * d),
+           "K/V rows need ld >= kv_heads * d, ld %% 8 == 0 and 16-byte alignment");
+  FQ_CHECK(q_dev == nullptr || (rows_ok(q_dev, ldq, cfg->h) && rows_ok(q_out_dev, ldqo, cfg->h)),
+           "Q rows need ldq, ldqo >= h, multiples of 8, and 16-byte alignment");
+  FQ_CHECK(q_dev == nullptr || q_dev != q_out_dev || ldq == ldqo, "rotating in place needs ldq == ldqo");
+  FQ_CUDA(launch_paged_append(pv, rv, rp, cfg->heads, d, cfg->kv_bits, static_cast<const __half*>(k_dev),
+                              static_cast<const __half*>(v_dev), ld, static_cast<const __half*>(q_dev), ldq,
+                              static_cast<__half*>(q_out_dev), ldqo, as_stream(stream)),
+          "paged append");
+  return FLEXQ_OK;
+}
+
+flexq_status flexq_paged_read(const flexq_config* cfg, const flexq_paged_kv* kv, const flexq_ragged* batch,
+                              void* k_out_dev, void* v_out_dev, int ld, void* stream) {
+  PagedView pv{};
+  RaggedView rv{};
+  FQ_TRY(check_paged(cfg, kv, batch, &pv, &rv));
+  if (rv.b == 0 || rv.rows == 0) return FLEXQ_OK;
+  const int d = cfg->h / cfg->heads;
+  FQ_CHECK(rows_ok(k_out_dev, ld, pv.kv_heads * d) && rows_ok(v_out_dev, ld, pv.kv_heads * d),
+           "K/V rows need ld >= kv_heads * d, ld %% 8 == 0 and 16-byte alignment");
+  FQ_CUDA(launch_paged_read(pv, rv, d, cfg->kv_bits, static_cast<__half*>(k_out_dev),
+                            static_cast<__half*>(v_out_dev), ld, as_stream(stream)),
+          "paged read");
+  return FLEXQ_OK;
+}
+
+flexq_status flexq_attention_paged(const flexq_config* cfg, const flexq_paged_kv* kv, const flexq_ragged* batch,
+                                   const void* q_dev, int ldq, void* out_dev, int ldo, void* stream) {
+  PagedView pv{};
+  RaggedView rv{};
+  FQ_TRY(check_paged(cfg, kv, batch, &pv, &rv));
+  if (rv.b == 0 || rv.rows == 0) return FLEXQ_OK;
+  FQ_CHECK(rows_ok(q_dev, ldq, cfg->h) && rows_ok(out_dev, ldo, cfg->h),
+           "q and out rows need ldq, ldo >= h, multiples of 8, and 16-byte alignment");
+  FQ_CHECK(q_dev != out_dev, "out may not alias q");
+  FQ_CUDA(launch_attn_paged(pv, rv, cfg->heads, cfg->h / cfg->heads, cfg->kv_bits,
+                            static_cast<const __half*>(q_dev), ldq, static_cast<__half*>(out_dev), ldo,
+                            as_stream(stream)),
+          "paged attention");
+  return FLEXQ_OK;
+}
+
 // --- layer steps ----------------------------------------------------------------
 size_t flexq_layer_workspace(const flexq_config* cfg, int rows, int mode) {
   if (check_config(cfg) != FLEXQ_OK || rows <= 0 || (mode != 0 && mode != 1)) return 0;

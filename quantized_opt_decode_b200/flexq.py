@@ -55,6 +55,20 @@ class flexq_kv(C.Structure):
                 ("max_len", C.c_int)]
 
 
+class flexq_paged_kv(C.Structure):
+    _fields_ = [("k", VP), ("v", VP), ("k_meta", VP), ("v_meta", VP), ("kv_heads", C.c_int), ("num_pages", C.c_int),
+                ("page_size", C.c_int), ("table_dev", VP), ("table_ld", C.c_int)]
+
+
+class flexq_ragged(C.Structure):
+    _fields_ = [("b", C.c_int), ("rows", C.c_int), ("max_new", C.c_int), ("max_len", C.c_int),
+                ("row_start_dev", VP), ("kv_len_dev", VP)]
+
+
+class flexq_rope(C.Structure):
+    _fields_ = [("cos_sin_dev", VP), ("max_pos", C.c_int), ("rot_dim", C.c_int), ("interleaved", C.c_int)]
+
+
 class flexq_model(C.Structure):
     _fields_ = [("cfg", flexq_config), ("layers", C.c_int), ("vocab", C.c_int),
                 ("max_pos", C.c_int), ("layer", C.POINTER(flexq_layer)),
@@ -77,6 +91,7 @@ class flexq_offload_choice(C.Structure):
 
 
 _CFG = C.POINTER(flexq_config)
+_PKV, _RAG = C.POINTER(flexq_paged_kv), C.POINTER(flexq_ragged)
 _SIGS = {
     "flexq_last_error": ([], C.c_char_p),
     "flexq_version": ([], C.c_int),
@@ -109,6 +124,13 @@ _SIGS = {
     "flexq_attention_prefill": ([_CFG, VP, C.c_int, C.c_int, C.c_int, VP, C.c_int, VP], C.c_int),
     "flexq_attention_prefill_cache": ([_CFG, C.POINTER(flexq_kv), VP, C.c_int, C.c_int, C.c_int, C.c_int, VP,
                                        C.c_int, VP], C.c_int),
+    "flexq_gemv_q4": ([VP, C.c_int, VP, C.c_int, C.c_int, C.c_int, VP, VP, C.c_int, C.c_int, VP, C.c_int, VP],
+                      C.c_int),
+    "flexq_paged_kv_bytes": ([_CFG, C.c_int, C.c_int, C.c_int], C.c_size_t),
+    "flexq_paged_append": ([_CFG, _PKV, _RAG, C.POINTER(flexq_rope), VP, VP, C.c_int, VP, C.c_int, VP, C.c_int,
+                            VP], C.c_int),
+    "flexq_paged_read": ([_CFG, _PKV, _RAG, VP, VP, C.c_int, VP], C.c_int),
+    "flexq_attention_paged": ([_CFG, _PKV, _RAG, VP, C.c_int, VP, C.c_int, VP], C.c_int),
     "flexq_layer_workspace": ([_CFG, C.c_int, C.c_int], C.c_size_t),
     "flexq_layer_prefill": ([_CFG, C.POINTER(flexq_layer), VP, VP, C.POINTER(flexq_kv), C.c_int,
                              C.c_int, VP, C.c_size_t, VP], C.c_int),
@@ -227,6 +249,11 @@ def flexq_linear_static_scratch(x, ldx, w, w_bits, m, n, k, bias, residual, ld_r
                                             force_splits, _s(stream)))
 
 
+def flexq_gemv_q4(x, ldx, w, m, n, k, bias, residual, ld_res, epilogue, y, ldy, stream=None):
+    _check(_lib.flexq_gemv_q4(_p(x), ldx, _p(w), m, n, k, _p(bias), _p(residual), ld_res, epilogue, _p(y), ldy,
+                              _s(stream)))
+
+
 def flexq_layernorm(x, ldx, gamma, beta, y, ldy, rows, h, eps=1e-5, stream=None):
     _check(_lib.flexq_layernorm(_p(x), ldx, _p(gamma), _p(beta), _p(y), ldy, rows, h, eps,
                                 _s(stream)))
@@ -259,6 +286,25 @@ def flexq_attention_prefill(cfg, qkv, ldqkv, b, s, out, ldo, stream=None):
 def flexq_attention_prefill_cache(cfg, kv, q, ldq, b, s, pos0, out, ldo, stream=None):
     _check(_lib.flexq_attention_prefill_cache(C.byref(cfg), C.byref(kv), _p(q), ldq, b, s, pos0, _p(out),
                                               ldo, _s(stream)))
+
+
+def flexq_paged_kv_bytes(cfg, kv_heads, num_pages, page_size) -> int:
+    return _lib.flexq_paged_kv_bytes(C.byref(cfg), kv_heads, num_pages, page_size)
+
+
+def flexq_paged_append(cfg, kv, batch, rope, k, v, ld, q=None, ldq=0, q_out=None, ldqo=0, stream=None):
+    _check(_lib.flexq_paged_append(C.byref(cfg), C.byref(kv), C.byref(batch),
+                                   C.byref(rope) if rope is not None else None, _p(k), _p(v), ld, _p(q), ldq,
+                                   _p(q_out), ldqo, _s(stream)))
+
+
+def flexq_paged_read(cfg, kv, batch, k_out, v_out, ld, stream=None):
+    _check(_lib.flexq_paged_read(C.byref(cfg), C.byref(kv), C.byref(batch), _p(k_out), _p(v_out), ld, _s(stream)))
+
+
+def flexq_attention_paged(cfg, kv, batch, q, ldq, out, ldo, stream=None):
+    _check(_lib.flexq_attention_paged(C.byref(cfg), C.byref(kv), C.byref(batch), _p(q), ldq, _p(out), ldo,
+                                      _s(stream)))
 
 
 def flexq_layer_workspace(cfg, rows, mode) -> int:
