@@ -207,6 +207,9 @@ cudaError_t launch_paged_read(const PagedView& kv, const RaggedView& batch, int 
                               __half* v_out, int ld, cudaStream_t s);
 cudaError_t launch_attn_paged(const PagedView& kv, const RaggedView& batch, int heads, int d, int kv_bits,
                               const __half* q, int ldq, __half* out, int ldo, cudaStream_t s);
+// Its sequences with at least min_rows query rows to a key/value head.
+cudaError_t launch_attn_paged_chunks(const PagedView& kv, const RaggedView& batch, int heads, int d, int kv_bits,
+                                     int min_rows, const __half* q, int ldq, __half* out, int ldo, cudaStream_t s);
 
 // Few-row product with a 4-bit tiled weight.
 constexpr int kGemvMaxRows = 16;
