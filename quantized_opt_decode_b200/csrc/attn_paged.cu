@@ -455,6 +455,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
     }
   }
   if (splits == 1) return;
+  __syncwarp();
   cluster.sync();
   for (int x = rank * kWarps * 32 + threadIdx.x; x < cols * D; x += splits * kWarps * 32) {
     const int c = x / D, e = x % D;
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
       }
     a.out[static_cast<size_t>(sp.row0 + c / g) * a.ldo + (head * g + c % g) * D + e] = __float2half_rn(acc / den);
   }
+  __syncwarp();
   cluster.sync();  // nobody leaves while another reads its shared memory
 }
 

@@ -754,6 +754,9 @@ flexq_status check_paged(const flexq_config* c, const flexq_paged_kv* kv, const 
                  (reinterpret_cast<uintptr_t>(batch->kv_len_dev) & 3) == 0,
              "row_start or kv_len is NULL or misaligned");
     FQ_CHECK(batch->max_new >= 1, "max_new must be >= 1");
+    FQ_CHECK(static_cast<long long>(batch->rows) * c->heads <= (1ll << 30) &&
+                 static_cast<long long>(batch->b) * kv->kv_heads <= (1ll << 24),
+             "rows * heads above 2^30 or b * kv_heads above 2^24 is not supported");
     FQ_CHECK(batch->max_len >= 1 && batch->max_len <= kMaxPagedLen, "max_len must be in 1..2^24");
     FQ_CHECK(kv->table_ld > 0 && static_cast<long long>(kv->table_ld) * kv->page_size >= batch->max_len,
              "max_len %d exceeds a table row (%d pages of %d)", batch->max_len, kv->table_ld, kv->page_size);
