@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   const int tiles = (sp.len + T::keys - 1) / T::keys;
   const int first = sp.len - sp.n;  // position of the first new token
   const int step = splits * kWarps;
-  const uint32_t ring = smem_u32(smem) + warp * T::stages * T::bytes;
+  uint8_t* ring = smem + warp * T::stages * T::bytes;
 
   // the lane's page of tile t (looked up one tile before its copies start)
   const int my_blk = (lane / T::lanes) * 8;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   int t_load = rank * kWarps + warp;
 #pragma unroll
   for (int s = 0; s < T::stages - 1; ++s) {
-    if (t_load < tiles) load_tile<D, Q4>(a.kv, head, t_load, page_for(t_load), ring + s * T::bytes, lane);
+    if (t_load < tiles) load_tile<D, Q4>(a.kv, head, t_load, page_for(t_load), smem_u32(ring + s * T::bytes), lane);
     cp_commit();
     t_load += step;
   }
@@ -213,14 +213,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
     {
       int to = slot + T::stages - 1;
       to = to >= T::stages ? to - T::stages : to;
-      if (t_load < tiles) load_tile<D, Q4>(a.kv, head, t_load, next_page, ring + to * T::bytes, lane);
+      if (t_load < tiles) load_tile<D, Q4>(a.kv, head, t_load, next_page, smem_u32(ring + to * T::bytes), lane);
       cp_commit();
       t_load += step;
       next_page = t_load < tiles ? page_for(t_load) : -1;
     }
-    const uint32_t st = ring + slot * T::bytes;
+    const uint8_t* st = ring + slot * T::bytes;
     slot = slot + 1 == T::stages ? 0 : slot + 1;
-    if (t * T::keys + T::keys > sp.len) clear_tail<D, Q4>(st, t, sp.len, lane);
+    if (t * T::keys + T::keys > sp.len) clear_tail<D, Q4>(smem_u32(st), t, sp.len, lane);
 
     // S^T: 16-key tile km holds blocks 2 km (rows r) and 2 km + 1 (rows r + 8)
     float s[KM][NT][4];
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int x = 2 * km + h, y = x + 4 * (r & 1);  // y: token in its block
-          const uint32_t kb = st + (r >> 1) * 8 * T::row;
+          const uint8_t* kb = st + (r >> 1) * 8 * T::row;
           const uint32_t ms = lds32(st + 2 * T::side + ((r >> 1) * 8 + y) * (D / 64) * 4 + (D == 128 ? (j >> 1) * 4 : 0));
           mn[h] = __low2half2(as_half2(ms));
           sc[h] = __high2half2(as_half2(ms));
@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
     if (Q4) {
       // lane (r, j): block j's words of dimensions 32 q + 4 r + {0..3}; 16-dimension
       // tile 2q + h is dimensions 32q + 4r + 2h (rows r) and + 1 (rows r + 8)
-      const uint32_t vb = st + T::side + j * 8 * T::row;
-      const uint32_t vm = st + 2 * T::side + T::meta + j * 8 * (D / 64) * 4;
+      const uint8_t* vb = st + T::side + j * 8 * T::row;
+      const uint8_t* vm = st + 2 * T::side + T::meta + j * 8 * (D / 64) * 4;
 #pragma unroll
       for (int gd = 0; gd < D / 64; ++gd) {
         __half2 sc[4], mn[4];
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t f[4];
         const int u = 2 * mt + ((lane >> 3) & 1);
-        ldmatrix4_trans(st + T::side + y * T::row + ((u ^ (y & 7)) * 16), f);
+        ldmatrix4_trans(smem_u32(st + T::side + y * T::row + ((u ^ (y & 7)) * 16)), f);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_16816(o[mt][nt], f[0], f[1], f[2], f[3], pt[nt][0], pt[nt][1]);
       }
