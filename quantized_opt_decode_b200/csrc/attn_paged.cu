@@ -20,6 +20,9 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
+#include <algorithm>
+#include <cstdlib>
+
 #include "paged.cuh"
 #include "warp_mma.cuh"
 
@@ -28,7 +31,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 4;
+constexpr int kMaxWarps = 8;
 constexpr int kMaxCluster = 8;
 
 struct PagedAttnArgs {
@@ -40,6 +43,8 @@ struct PagedAttnArgs {
   __half* out;
   int ldo;
   float scale_log2;
+  float slack;        // 8 / scale_log2
+  uint32_t by_group;  // c / group = (c * by_group) >> 16 for the columns c < 16
   uint32_t* err;
 };
 
@@ -122,7 +127,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
 template <int D, bool Q4, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_kernel(const PagedAttnArgs a) {
+__global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const PagedAttnArgs a) {
   using T = Tile<D, Q4>;
   constexpr int NC = 8 * NT;       // columns: query rows
   constexpr int DL = D / 4;        // dimensions of Q and K that a lane holds
@@ -130,12 +135,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   constexpr int MT = D / 16;       // 16-dimension tiles of the output
   constexpr int KM = T::keys / 16; // 16-key tiles
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float s_m[kWarps][NC], s_l[kWarps][NC];
+  __shared__ float s_m[kMaxWarps][NC], s_l[kMaxWarps][NC];
   __shared__ float c_m[NC], c_l[NC];
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
   const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  const int lane = static_cast<int>(lane_id()), warp = threadIdx.x >> 5;
+  const int lane = static_cast<int>(lane_id()), warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int r = lane >> 2, j = lane & 3;
   const int unit = blockIdx.x / splits;
   const int i = unit / a.kv.kv_heads, head = unit % a.kv.kv_heads;
@@ -145,7 +150,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   if (sp.n == 0 || cols > NC) return;  // (every CTA of the cluster alike)
   const int tiles = (sp.len + T::keys - 1) / T::keys;
   const int first = sp.len - sp.n;  // position of the first new token
-  const int step = splits * kWarps;
+  const int step = splits * warps;
+  auto token_of = [&](int c) { return static_cast<int>((c * a.by_group) >> 16); };
   uint8_t* ring = smem + warp * T::stages * T::bytes;
 
   // the lane's page of tile t (looked up one tile before its copies start)
@@ -154,7 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
     const int p = t * T::keys + my_blk;
     return p < sp.len ? page_of(a.kv, i, p, a.err) : -1;
   };
-  int t_load = rank * kWarps + warp;
+  int t_load = rank * warps + warp;
 #pragma unroll
   for (int s = 0; s < T::stages - 1; ++s) {
     if (t_load < tiles) load_tile<D, Q4>(a.kv, head, t_load, page_for(t_load), smem_u32(ring + s * T::bytes), lane);
@@ -169,8 +175,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   for (int nt = 0; nt < NT; ++nt) {
     const int c = nt * 8 + r;
     const bool live = c < cols;
-    const __half* src = a.q + static_cast<size_t>(sp.row0 + (live ? c / g : 0)) * a.ldq +
-                        (head * g + (live ? c % g : 0)) * D + j * DL;
+    const int tok = live ? token_of(c) : 0, hq = live ? c - tok * g : 0;
+    const __half* src = a.q + static_cast<size_t>(sp.row0 + tok) * a.ldq + (head * g + hq) * D + j * DL;
 #pragma unroll
     for (int w = 0; w < WL; ++w) {
       uint4 v = *reinterpret_cast<const uint4*>(src + w * 8);
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   }
 
   float o[MT][NT][4];
-  float mx[NT][2], sum[NT][2];
+  float mx[NT][2], off[NT][2], sum[NT][2];  // base of the exponents (raw score), -base * scale, sum of weights
   int last[NT][2];  // position of the lane's two rows of each column tile
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -201,13 +207,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       mx[nt][e] = -INFINITY;
+      off[nt][e] = 0.f;
       sum[nt][e] = 0.f;
-      last[nt][e] = first + min((nt * 8 + 2 * j + e) / g, sp.n - 1);
+      last[nt][e] = first + min(token_of(nt * 8 + 2 * j + e), sp.n - 1);
     }
   }
 
   int slot = 0;
-  for (int t = rank * kWarps + warp; t < tiles; t += step) {
+  for (int t = rank * warps + warp; t < tiles; t += step) {
     cp_wait<T::stages - 2>();
     __syncwarp();
     {
@@ -295,49 +302,54 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
             if (p > last[nt][e & 1]) s[km][nt][e] = -INFINITY;
         }
     }
+    // The exponent base of a row only moves when a score outgrows it by 2^8, so that O is
+    // rarely rescaled; the weights stay below 2^8 in fp16 (a relative rounding, 2^-11,
+    // wherever the base is; the sum keeps fp32).
     uint32_t pt[NT][2 * KM];
+    float tm[NT][2];
     bool grew = false;
-    float alpha[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float tm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int km = 0; km < KM; ++km)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tm[e & 1] = fmaxf(tm[e & 1], s[km][nt][e]);
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        float m = -INFINITY;
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], x));
-        const float m = fmaxf(mx[nt][e], tm[e]);
-        const float base = m == -INFINITY ? 0.f : m * a.scale_log2;  // no key of the row so far
-        alpha[nt][e] = exp2_approx(mx[nt][e] * a.scale_log2 - base);
-        grew |= m > mx[nt][e];
-        mx[nt][e] = m;
-        float add = 0.f;
-#pragma unroll
-        for (int km = 0; km < KM; ++km) {
-          s[km][nt][e] = exp2_approx(s[km][nt][e] * a.scale_log2 - base);
-          s[km][nt][e + 2] = exp2_approx(s[km][nt][e + 2] * a.scale_log2 - base);
-          add += s[km][nt][e] + s[km][nt][e + 2];
-        }
-        sum[nt][e] = sum[nt][e] * alpha[nt][e] + add;
+        for (int km = 0; km < KM; ++km) m = fmaxf(m, fmaxf(s[km][nt][e], s[km][nt][e + 2]));
+        tm[nt][e] = m;
+        grew |= m > mx[nt][e] + a.slack;  // (from -inf: any finite score)
       }
+    if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = tm[nt][e];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+          m = m > mx[nt][e] + a.slack ? m : mx[nt][e];
+          alpha[e] = m == -INFINITY ? 1.f : exp2_approx((mx[nt][e] - m) * a.scale_log2);
+          mx[nt][e] = m;
+          off[nt][e] = m == -INFINITY ? 0.f : -m * a.scale_log2;  // no key of the row so far: 0
+          sum[nt][e] *= alpha[e];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= alpha[e & 1];
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int km = 0; km < KM; ++km) {
-        // weights in fp16 for the product (relative 2^-11; the sum keeps fp32)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[km][nt][e] = exp2_approx(fmaf(s[km][nt][e], a.scale_log2, off[nt][e & 1]));
+        sum[nt][0] += s[km][nt][0] + s[km][nt][2];
+        sum[nt][1] += s[km][nt][1] + s[km][nt][3];
         pt[nt][2 * km] = movmatrix_trans(pack_half2(s[km][nt][0], s[km][nt][1]));
         pt[nt][2 * km + 1] = movmatrix_trans(pack_half2(s[km][nt][2], s[km][nt][3]));
       }
-    }
-    if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= alpha[nt][e & 1];
-    }
 
     // O^T += V^T P^T
     if (Q4) {
@@ -432,20 +444,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   __syncthreads();
   auto weight = [&](float m, float top) { return m == -INFINITY ? 0.f : exp2_approx((m - top) * a.scale_log2); };
   float* joined = reinterpret_cast<float*>(smem);  // over the first warp's part, element by element
-  for (int x = threadIdx.x; x < cols * D; x += kWarps * 32) {
+  for (int x = threadIdx.x; x < cols * D; x += warps * 32) {
     const int c = x / D, e = x % D;
     float top = s_m[0][c];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][c]);
+    for (int w = 1; w < warps; ++w) top = fmaxf(top, s_m[w][c]);
     float acc = 0.f, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const float f = weight(s_m[w][c], top);
       acc += f * reinterpret_cast<const float*>(smem + w * T::stages * T::bytes)[x];
       l += f * s_l[w][c];
     }
     if (splits == 1) {
-      a.out[static_cast<size_t>(sp.row0 + c / g) * a.ldo + (head * g + c % g) * D + e] = __float2half_rn(acc / l);
+      a.out[static_cast<size_t>(sp.row0 + token_of(c)) * a.ldo + (head * g + c - token_of(c) * g) * D + e] = __float2half_rn(acc / l);
     } else {
       joined[x] = acc;
       if (e == 0) {
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
   if (splits == 1) return;
   __syncwarp();
   cluster.sync();
-  for (int x = rank * kWarps * 32 + threadIdx.x; x < cols * D; x += splits * kWarps * 32) {
+  for (int x = rank * warps * 32 + threadIdx.x; x < cols * D; x += splits * warps * 32) {
     const int c = x / D, e = x % D;
     float top = -INFINITY, part[kMaxCluster], m[kMaxCluster], l[kMaxCluster];
 #pragma unroll
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
         acc += f * part[k];
         den += f * l[k];
       }
-    a.out[static_cast<size_t>(sp.row0 + c / g) * a.ldo + (head * g + c % g) * D + e] = __float2half_rn(acc / den);
+    a.out[static_cast<size_t>(sp.row0 + token_of(c)) * a.ldo + (head * g + c - token_of(c) * g) * D + e] = __float2half_rn(acc / den);
   }
   __syncwarp();
   cluster.sync();  // nobody leaves while another reads its shared memory
@@ -485,19 +495,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) attn_paged_rows_
 template <int D, bool Q4, int NT>
 cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   using T = Tile<D, Q4>;
-  constexpr int smem = kWarps * T::stages * T::bytes;
   static_assert(T::stages * T::bytes >= 8 * NT * D * 4, "a warp's ring holds its partial output");
-  cudaError_t e = allow_smem<attn_paged_rows_kernel<D, Q4, NT>>(smem);
+  cudaError_t e = allow_smem<attn_paged_rows_kernel<D, Q4, NT>>(kMaxWarps * T::stages * T::bytes);
   if (e != cudaSuccess) return e;
+  // Warps of a unit (its tiles go round them): what 16 warps an SM give it, but no more
+  // than it has tiles; two at least, so that a unit's fixed cost is shared.
   const long long units = static_cast<long long>(a.batch.b) * a.kv.kv_heads;
-  // share a history out over a cluster until every SM has three CTAs, down to a tile a warp
-  int splits = 1;
-  while (splits < kMaxCluster && units * splits < 3ll * runtime().num_sms &&
-         a.batch.max_len > splits * kWarps * T::keys)
-    splits *= 2;
+  const long long tiles = (a.batch.max_len + T::keys - 1) / T::keys;
+  const long long ways = std::min(16ll * runtime().num_sms / units, tiles);
+  int warps = ways >= 8 ? 8 : ways >= 4 ? 4 : 2;
+  if (getenv("FQ_WARPS")) warps = atoi(getenv("FQ_WARPS"));
+  const int splits = static_cast<int>(std::max(1ll, std::min<long long>(kMaxCluster, ways / warps)));
+  const int smem = warps * T::stages * T::bytes;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(warps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -529,8 +541,12 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attn_paged(const PagedView& kv, const RaggedView& batch, int heads, int d, int kv_bits,
                               const __half* q, int ldq, __half* out, int ldo, cudaStream_t s) {
-  PagedAttnArgs a{kv,  batch, heads, heads / kv.kv_heads, q, ldq,
-                  out, ldo,   1.4426950408889634f / sqrtf(static_cast<float>(d)), runtime().err};
+  const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(d));
+  const int group = heads / kv.kv_heads;
+  // ceil(2^16 / group): exact quotients for c < 16, group <= 16 (the error c * group / 2^16 stays below 1 / group)
+  const PagedAttnArgs a{kv,  batch, heads,      group,           q,
+                        ldq, out,   ldo,        scale_log2,      8.f / scale_log2,
+                        static_cast<uint32_t>((65536 + group - 1) / group), runtime().err};
   if (kv_bits == 4) return d == 128 ? launch_d<128, true>(a, s) : launch_d<64, true>(a, s);
   return d == 128 ? launch_d<128, false>(a, s) : launch_d<64, false>(a, s);
 }

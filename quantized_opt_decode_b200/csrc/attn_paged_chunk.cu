@@ -12,7 +12,7 @@
 //                    exponent base only moves when a row outgrows it by 2^8: P then stays
 //                    below 2^8 in fp16 (a relative rounding, so the base does not
 //                    matter), and O is rescaled rarely;
-//   warps 8-15       bring K and V: pages looked up, codes fetched a tile ahead
+//   warps 8-11       bring K and V: pages looked up, codes fetched a tile ahead
 //                    into registers, dequantized (rounded once to fp16, as the codec's
 //                    values) and stored in the 128-byte-swizzled layout; a
 //                    word of codes is one 16-byte store, since the orders of the head's
@@ -21,13 +21,18 @@
 //                    loaded, keys y, y + 4 of a block lie side by side, and O's columns
 //                    are unscrambled when they are stored.  V of an fp16 cache is
 //                    transposed 8 x 8 in registers;
-//   warp 16          issues the products: while row tile 0 is in its softmax,
-//                    row tile 1's products run.
-// A long history of few units is shared out over a cluster of CTAs, whose
+//   warp 12          issues the products, row tile 0's and row tile 1's by turns: while
+//                    one is in its softmax, the other's run.
+// One CTA an SM walks the units (256 query rows of a sequence and key/value head) that fall to it:
+// every role runs on into the next unit on its own, so the stores of one unit overlap the
+// products of the next; unit numbers that hold no rows (paged_math.h) cost a lane of a search,
+// not a CTA.  A long history of few units is shared out over a cluster of CTAs, whose
 // (maximum, sum, O) are joined over distributed shared memory in a fixed order.
 // Every wait is bounded; on expiry the error word is set and the CTA unwinds.
 #include <cooperative_groups.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "paged.cuh"
 #include "warp_mma.cuh"
@@ -41,7 +46,7 @@ constexpr int kRowShift = 8;  // 256 query rows of a unit
 constexpr int kRows = 1 << kRowShift;
 constexpr int kKeys = 128;
 constexpr int kStages = 2;
-constexpr int kSoftmaxWarps = 8, kLoadWarps = 8;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kMaxCluster = 8;
@@ -74,34 +79,111 @@ struct Layout {
 };
 
 struct Barriers {
-  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], s_full[2], p_full[2], done;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2];  // by row tile
+  uint64_t done;
   uint32_t tmem;
 };
 
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+// 256 query rows of one sequence and key/value head.
+struct Unit {
+  int i, head, row0, first, len, c0, rows;
+  int tiles;  // key tiles that some row of the unit sees
+};
+
+// The units of CTA (or cluster) `id` of `count`, in order: numbers id, id + count, ..,
+// 32 looked up at a time, one by each lane; those that hold no rows are passed over.
+struct UnitWalk {
+  long long base, total, stride;
+  uint32_t found;
+  int i, head, row0, n, len, c0;
+
+  __device__ __forceinline__ void start(const ChunkArgs& a, int id, int count) {
+    total = unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1) * a.kv.kv_heads;
+    stride = count;
+    base = id;
+    found = 0;
+  }
+  // Every lane of the warp calls this and gets the same unit; false: no more.
+  __device__ __forceinline__ bool next(const ChunkArgs& a, Unit& out) {
+    while (found == 0) {
+      if (base >= total) return false;
+      const long long w = base + stride * static_cast<int>(lane_id());
+      base += stride * 32;
+      found = __ballot_sync(0xffffffffu, w < total && look(a, static_cast<int>(w)));
+    }
+    const int from = __ffs(found) - 1;
+    found &= found - 1;
+    const int g = a.group;
+    out.i = __shfl_sync(0xffffffffu, i, from);
+    out.head = __shfl_sync(0xffffffffu, head, from);
+    out.row0 = __shfl_sync(0xffffffffu, row0, from);
+    out.len = __shfl_sync(0xffffffffu, len, from);
+    out.c0 = __shfl_sync(0xffffffffu, c0, from);
+    const int tokens = __shfl_sync(0xffffffffu, n, from);
+    out.first = out.len - tokens;
+    out.rows = min(kRows, tokens * g - out.c0);
+    out.tiles = (out.first + (out.c0 + out.rows - 1) / g + kKeys) / kKeys;
+    return true;
+  }
+  __device__ __forceinline__ bool look(const ChunkArgs& a, int w) {
+    const int g = a.group, u = w / a.kv.kv_heads;
+    head = w - u * a.kv.kv_heads;
+    int lo = 0, hi = a.batch.b;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (unit_base(a.batch, mid, g, kRowShift, 1) <= u) lo = mid; else hi = mid;
+    }
+    i = lo;
+    const Span sp = ragged_span(a.batch, i, a.err);
+    row0 = sp.row0;
+    n = sp.n;
+    len = sp.len;
+    const int rows = sp.n * g;  // at most max_new * group, which the entry point bounds
+    const int rel = u - static_cast<int>(unit_base(a.batch, i, g, kRowShift, 1));
+    const int units = (rows + kRows - 1) / kRows;
+    c0 = (units - 1 - rel) * kRows;  // the later rows, which see more keys, first
+    return sp.n > 0 && rows >= a.min_rows && rel >= 0 && rel < units;
+  }
+};
+
+// Load and wait in one statement, so that no use of the registers can move ahead of the wait.
+__device__ __forceinline__ void tmem_read_x32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
 
-// Waits for the loads issued so far; naming the registers keeps their uses behind it.
-__device__ __forceinline__ void tmem_wait_x32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
+__device__ __forceinline__ void tmem_read_x64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, "
+      "%40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
+      "%59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+        "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]),
+        "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]),
+        "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]),
+        "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
 }
 
-// One asm of load and wait for eight columns.
 __device__ __forceinline__ void tmem_read_x8(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
@@ -111,13 +193,38 @@ __device__ __forceinline__ void tmem_read_x8(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+// One lane of the converged warp, always the same; the compiler then keeps the
+// descriptors of the products it issues in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(lo), "r"(hi));
+  return x;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -232,48 +339,62 @@ template <int D>
 struct Loader<D, false> {
   static constexpr int lanes = D / 8;  // lanes of a block: 16 bytes of each of its eight keys
   static constexpr int per_warp = 32 / lanes;
-  uint4 k[8], v[8];
-  int page;
+  static constexpr int NQ = kKeys / 8 / (kLoadWarps * per_warp);
+  uint4 v[NQ][8];
+  int page[NQ];
   int warp, lane, sub, len;
 
-  __device__ __forceinline__ int block() const { return warp * per_warp + lane / lanes; }
-  __device__ __forceinline__ bool mine() const { return block() < kKeys / 8; }
+  __device__ __forceinline__ int block(int q) const { return (q * kLoadWarps + warp) * per_warp + lane / lanes; }
   __device__ __forceinline__ void look_up(const ChunkArgs& a, int i, int t) {
-    const int p = t * kKeys + block() * 8;
-    page = mine() && p < len ? page_of(a.kv, i, p, a.err) : -1;
-  }
-  __device__ __forceinline__ void fetch(const ChunkArgs& a, const void* pool, int head, int t, uint4 (&x)[8]) const {
-    const int p = t * kKeys + block() * 8;
-    const size_t slot = page >= 0 ? pool_slot(a.kv, page, head, p) : 0;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      x[y] = make_uint4(0u, 0u, 0u, 0u);
-      if (page >= 0 && p + y < len) x[y] = ldg128(static_cast<const char*>(pool) + (slot + y) * (D * 2) + sub * 16);
+    for (int q = 0; q < NQ; ++q) {
+      const int p = t * kKeys + block(q) * 8;
+      page[q] = p < len ? page_of(a.kv, i, p, a.err) : -1;
     }
   }
-  __device__ __forceinline__ void fetch_k(const ChunkArgs& a, int head, int t) { fetch(a, a.kv.k, head, t, k); }
-  __device__ __forceinline__ void fetch_v(const ChunkArgs& a, int head, int t) { fetch(a, a.kv.v, head, t, v); }
-  __device__ __forceinline__ void store_k(uint32_t st) const {
-    if (!mine()) return;
+  // K straight into its swizzled place; rows behind the end are zeros.
+  __device__ __forceinline__ void copy_k(const ChunkArgs& a, int head, int t, uint32_t st) const {
 #pragma unroll
-    for (int y = 0; y < 8; ++y)
-      sts128(st + (sub >> 3) * (kKeys * 128) + sw128(block() * 8 + y, sub & 7), k[y].x, k[y].y, k[y].z, k[y].w);
+    for (int q = 0; q < NQ; ++q) {
+      const int p = t * kKeys + block(q) * 8;
+      const size_t slot = page[q] >= 0 ? pool_slot(a.kv, page[q], head, p) : 0;
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        cp_async16(st + (sub >> 3) * (kKeys * 128) + sw128(block(q) * 8 + y, sub & 7),
+                   static_cast<const char*>(a.kv.k) + (slot + y) * (D * 2) + sub * 16, page[q] >= 0 && p + y < len);
+    }
+    cp_commit();
+  }
+  __device__ __forceinline__ void fetch_v(const ChunkArgs& a, int head, int t) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int p = t * kKeys + block(q) * 8;
+      const size_t slot = page[q] >= 0 ? pool_slot(a.kv, page[q], head, p) : 0;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        v[q][y] = make_uint4(0u, 0u, 0u, 0u);
+        if (page[q] >= 0 && p + y < len)
+          v[q][y] = ldg128(static_cast<const char*>(a.kv.v) + (slot + y) * (D * 2) + sub * 16);
+      }
+    }
   }
   __device__ __forceinline__ void store_v(uint32_t st) const {
-    if (!mine()) return;
-    const int blk = block();
-    const uint32_t base = st + (blk >> 3) * (D * 128);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t o[4];
+    for (int q = 0; q < NQ; ++q) {
+      const int blk = block(q);
+      const uint32_t base = st + (blk >> 3) * (D * 128);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const uint4 &lo = v[2 * y], &hi = v[2 * y + 1];
-        const uint32_t x0 = e < 2 ? lo.x : e < 4 ? lo.y : e < 6 ? lo.z : lo.w;
-        const uint32_t x1 = e < 2 ? hi.x : e < 4 ? hi.y : e < 6 ? hi.z : hi.w;
-        o[y] = __byte_perm(x0, x1, (e & 1) ? 0x7632 : 0x5410);
+      for (int e = 0; e < 8; ++e) {
+        uint32_t o[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint4 &lo = v[q][2 * y], &hi = v[q][2 * y + 1];
+          const uint32_t x0 = e < 2 ? lo.x : e < 4 ? lo.y : e < 6 ? lo.z : lo.w;
+          const uint32_t x1 = e < 2 ? hi.x : e < 4 ? hi.y : e < 6 ? hi.z : hi.w;
+          o[y] = __byte_perm(x0, x1, (e & 1) ? 0x7632 : 0x5410);
+        }
+        sts128(base + sw128((D / 8) * e + sub, blk & 7), o[0], o[1], o[2], o[3]);  // dimension 8 sub + e
       }
-      sts128(base + sw128((D / 8) * e + sub, blk & 7), o[0], o[1], o[2], o[3]);  // dimension 8 sub + e
     }
   }
 };
@@ -289,31 +410,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
   const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  const int lane = static_cast<int>(lane_id()), warp = threadIdx.x >> 5;
-
-  // the unit: 256 query rows of one sequence and key/value head, the later rows first
-  const int work = blockIdx.x / splits;
-  const int head = work % a.kv.kv_heads, u = work / a.kv.kv_heads;
+  const int lane = static_cast<int>(lane_id());
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
   const int g = a.group;
-  const int i = find_unit_owner(a.batch, u, g, kRowShift, 1);
-  if (i < 0) return;
-  const Span sp = ragged_span(a.batch, i, a.err);
-  const int total = sp.n * g;  // at most max_new * group, checked by the launcher
-  const int rel = u - static_cast<int>(unit_base(a.batch, i, g, kRowShift, 1));
-  const int units = (total + kRows - 1) / kRows;
-  if (sp.n == 0 || total < a.min_rows || rel < 0 || rel >= units) return;  // (all CTAs of a cluster alike)
-  const int c0 = (units - 1 - rel) * kRows;
-  const int rows = min(kRows, total - c0);
-  const int mtiles = rows > 128 ? 2 : 1;
-  const int first = sp.len - sp.n;
-  const int keys = first + (c0 + rows - 1) / g + 1;  // keys that some row of the unit sees
-  const int all = (keys + kKeys - 1) / kKeys;
-  const int mine = all > rank ? (all - rank + splits - 1) / splits : 0;  // tiles rank, rank + splits, ..
+  // With a history shared out over a cluster, a cluster has one unit number.
+  UnitWalk walk;
+  Unit un;
+  walk.start(a, blockIdx.x / splits, gridDim.x / splits);
+  if (!walk.next(a, un)) return;  // (every warp of the cluster alike)
 
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   if (threadIdx.x == 0) {
-    mbar_init(&bar.q_full, kSoftmaxWarps);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bar.k_full[s], kLoadWarps);
       mbar_init(&bar.v_full[s], kLoadWarps);
@@ -321,8 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       mbar_init(&bar.v_empty[s], 1);
     }
     for (int m = 0; m < 2; ++m) {
+      mbar_init(&bar.q_full[m], 4);
       mbar_init(&bar.s_full[m], 1);
       mbar_init(&bar.p_full[m], 4);
+      mbar_init(&bar.o_full[m], 1);
+      mbar_init(&bar.o_free[m], 4);
     }
     mbar_init(&bar.done, 1);
     s_fail = 0;
@@ -335,125 +446,151 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   auto wait = [&](uint64_t* b, uint32_t parity, uint32_t code) {
     if (mbar_wait(b, parity, a.limit_ns)) return true;
     set_error(a.err, code);
     atomicExch(&s_fail, 1);
     return false;
   };
+  // key tiles of this CTA: rank, rank + splits, ..
+  auto tiles_of = [&](const Unit& x) { return x.tiles > rank ? (x.tiles - rank + splits - 1) / splits : 0; };
 
   if (warp < kSoftmaxWarps) {
     // --- softmax of one row -------------------------------------------------------
-    const int m = warp >> 2, row = threadIdx.x;  // row of the unit: lane row % 128 of tile m
+    const int m = warp >> 2, row = threadIdx.x;  // row of the unit: TMEM lane row % 128 of row tile m
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + m * 128, o_col = tmem + lanes + 256 + m * D;
-    const bool live = row < rows;
-    const int c = c0 + (live ? row : 0);
-    {
-      const __half* src = a.q + static_cast<size_t>(sp.row0 + c / g) * a.ldq + (head * g + c % g) * D;
+    const float slack = 8.f / a.scale_log2;
+    // Q's row into its swizzled place (every product that read the last one has completed)
+    auto load_q = [&](const Unit& x) {
+      const bool live = row < x.rows;
+      const int c = x.c0 + (live ? row : 0), tok = c / g;
+      const __half* src = a.q + static_cast<size_t>(x.row0 + tok) * a.ldq + (x.head * g + c - tok * g) * D;
       const uint32_t dst = sbase + m * L::q_tile;
 #pragma unroll
       for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 x = live ? *reinterpret_cast<const uint4*>(src + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = live ? *reinterpret_cast<const uint4*>(src + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t at = dst + (ch >> 3) * (128 * 128) + sw128(row & 127, ch & 7);
         if (Q4)  // (e, e + 4)
-          sts128(at, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
-                 __byte_perm(x.y, x.w, 0x7632));
+          sts128(at, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                 __byte_perm(v.y, v.w, 0x7632));
         else
-          sts128(at, x.x, x.y, x.z, x.w);
+          sts128(at, v.x, v.y, v.z, v.w);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.q_full);
-    }
-    const int pos = live ? first + c / g : keys - 1;
-    float base = -INFINITY, sum = 0.f;  // base: exponent base in units of the raw scores
-    const float slack = 8.f / a.scale_log2;
-    bool ok = true;
-    if (m < mtiles) {
+      if (lane == 0) mbar_arrive(&bar.q_full[m]);
+    };
+    bool more = true, ok = true;
+    while (more && m * 128 >= un.rows) more = walk.next(a, un);  // row tile 1: units that have one
+    if (more) load_q(un);
+    uint32_t s_phase = 0, o_phase = 0;
+    while (more) {
+      const Unit cur = un;
+      const bool live = row < cur.rows;
+      const int c = cur.c0 + (live ? row : 0), tok = c / g;
+      const int pos = live ? cur.first + tok : cur.len;
+      const int mine = tiles_of(cur);
+      float base = -INFINITY;  // exponent base, a raw score
+      uint64_t sum = 0;        // sums of the even and the odd columns' weights
       for (int it = 0; it < mine; ++it) {
-        if (!(ok = __all_sync(0xffffffffu, wait(&bar.s_full[m], it & 1, DEV_TIMEOUT_EPILOGUE)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait(&bar.s_full[m], s_phase, DEV_TIMEOUT_EPILOGUE)))) break;
+        s_phase ^= 1;
         tc_fence_after();
-        const int p0 = (rank + it * splits) * kKeys;
-        const int lim = pos - p0;  // tokens 0 .. lim of the tile count
+        const int lim = pos - (rank + it * splits) * kKeys;  // tokens 0 .. lim of the tile count
         const bool masked = __any_sync(0xffffffffu, lim < kKeys - 1);
         float top = -INFINITY;
-        uint32_t s[2][32];
-        tmem_ld_x32(s_col, s[0]);
+        if (!masked) {
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[64];
+            tmem_read_x64(s_col + 64 * h, s);
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tmem_wait_x32(s[ch & 1]);
-          if (ch < 3) tmem_ld_x32(s_col + 32 * (ch + 1), s[(ch + 1) & 1]);
-          if (masked) {
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                t4[k] = max3(t4[k], __uint_as_float(s[e + 2 * k]), __uint_as_float(s[e + 2 * k + 1]));
+          }
+          top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+        } else {
+          // the scores behind the row's position leave S here
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t s[32];
+            tmem_read_x32(s_col + 32 * ch, s);
+            const int here = lim - 32 * ch;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const int tok = 32 * ch + (Q4 ? (e & ~7) + ((e & 7) >> 1) + 4 * (e & 1) : e);
-              if (tok <= lim) top = fmaxf(top, __uint_as_float(s[ch & 1][e]));
+              const int t = Q4 ? (e & ~7) + ((e & 7) >> 1) + 4 * (e & 1) : e;
+              if (t > here) s[e] = 0xff800000u;
+              top = fmaxf(top, __uint_as_float(s[e]));
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[ch & 1][e]));
+            tmem_st_x32(s_col + 32 * ch, s);
           }
+          tmem_st_wait();
         }
         const bool move = top > base + slack;  // (from -inf: any finite score)
         if (__any_sync(0xffffffffu, move)) {
           const float nb = move ? top : base;
           const float alpha = base == -INFINITY ? 0.f : exp2_approx((base - nb) * a.scale_log2);
           base = nb;
-          sum *= alpha;
+          float s0, s1;
+          unpair(sum, s0, s1);
+          sum = pair(__float_as_uint(s0 * alpha), __float_as_uint(s1 * alpha));
           if (it > 0) {
-            const float f = alpha;
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
-              tmem_ld_x32(o_col + 32 * ch, s[0]);
-              tmem_wait_x32(s[0]);
+              uint32_t o[32];
+              tmem_read_x32(o_col + 32 * ch, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[0][e] = __float_as_uint(__uint_as_float(s[0][e]) * f);
-              tmem_st_x32(o_col + 32 * ch, s[0]);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st_x32(o_col + 32 * ch, o);
             }
           }
         }
-        const float off = base == -INFINITY ? 0.f : -base * a.scale_log2;
-        tmem_ld_x32(s_col, s[0]);
+        const uint32_t off = __float_as_uint(base == -INFINITY ? 0.f : -base * a.scale_log2);
+        const uint64_t off2 = pair(off, off), scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
+        uint64_t sums[4] = {sum, 0, 0, 0};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[64], p[32];
+          tmem_read_x64(s_col + 64 * h, s);
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tmem_wait_x32(s[ch & 1]);
-          if (ch < 3) tmem_ld_x32(s_col + 32 * (ch + 1), s[(ch + 1) & 1]);
-          uint32_t p[16];
-          float add[2] = {0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x0 = fmaf(__uint_as_float(s[ch & 1][e]), a.scale_log2, off);
-            float x1 = fmaf(__uint_as_float(s[ch & 1][e + 1]), a.scale_log2, off);
-            if (masked) {
-              const int t0 = 32 * ch + (Q4 ? (e & ~7) + ((e & 7) >> 1) : e);
-              if (t0 > lim) x0 = -INFINITY;
-              if (t0 + (Q4 ? 4 : 1) > lim) x1 = -INFINITY;
-            }
+          for (int e = 0; e < 64; e += 2) {
+            float x0, x1;
+            unpair(fma2(pair(s[e], s[e + 1]), scale2, off2), x0, x1);
             x0 = exp2_approx(x0);
             x1 = exp2_approx(x1);
-            add[0] += x0;
-            add[1] += x1;
+            sums[(e / 2) & 3] = add2(sums[(e / 2) & 3], pair(__float_as_uint(x0), __float_as_uint(x1)));
             p[e / 2] = pack_half2(x0, x1);
           }
-          sum += add[0] + add[1];
-          // over S's columns 16 ch .. 16 ch + 15, which are read already (the load
-          // in flight is of columns 32 (ch + 1) and up)
-          tmem_st_x16(s_col + 16 * ch, p);
+          // over S's columns 32 h .. 32 h + 31, which are read already
+          tmem_st_x32(s_col + 32 * h, p);
         }
+        sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[m]);
       }
-    }
-    ok = ok && __all_sync(0xffffffffu, wait(&bar.done, 0, DEV_TIMEOUT_EPILOGUE));
-    tc_fence_after();
-    if (ok && m < mtiles) {
+      if (!ok) break;
+      do more = walk.next(a, un);
+      while (more && m * 128 >= un.rows);
+      if (more) load_q(un);
+
+      ok = __all_sync(0xffffffffu, wait(&bar.o_full[m], o_phase, DEV_TIMEOUT_EPILOGUE));
+      if (ok && splits > 1 && cur.rows > 128)  // the parts are laid over K and V: wait for both row tiles
+        ok = __all_sync(0xffffffffu, wait(&bar.o_full[m ^ 1], 0, DEV_TIMEOUT_EPILOGUE));
+      if (!ok) break;
+      o_phase ^= 1;
+      tc_fence_after();
+      float s0, s1;
+      unpair(sum, s0, s1);
       if (splits == 1) {
-        const float inv = 1.f / sum;
-        __half* dst = a.out + static_cast<size_t>(sp.row0 + c / g) * a.ldo + (head * g + c % g) * D;
+        const float inv = 1.f / (s0 + s1);
+        __half* dst = a.out + static_cast<size_t>(cur.row0 + tok) * a.ldo + (cur.head * g + c - tok * g) * D;
 #pragma unroll 1
         for (int u0 = 0; u0 < D / W; u0 += 8) {
           uint32_t o[W][8];
@@ -471,11 +608,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
             }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.o_free[m]);
       } else {
         s_m[row] = base;
-        s_l[row] = sum;
-        // column order, 16-byte units XORed by the row: over the K and V stages, which
-        // no product reads any more
+        s_l[row] = s0 + s1;
+        // in O's column order, 16-byte units XORed by the row
 #pragma unroll 1
         for (int q = 0; q < D; q += 8) {
           uint32_t o[8];
@@ -497,78 +636,146 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     ld.warp = warp - kSoftmaxWarps;
     ld.lane = lane;
     ld.sub = lane % Loader<D, Q4>::lanes;
-    ld.len = sp.len;
-    if (mine > 0) {
-      ld.look_up(a, i, rank);
-      ld.fetch_k(a, head, rank);
-      ld.fetch_v(a, head, rank);
+    int n = 0;  // tiles so far
+    bool more = true;
+    int it = 0, mine = tiles_of(un);
+    while (more && mine == 0) {
+      more = walk.next(a, un);
+      if (more) mine = tiles_of(un);
     }
-    for (int it = 0; it < mine; ++it) {
-      const int st = it % kStages, next = rank + (it + 1) * splits;
-      const uint32_t free_parity = ((it / kStages) & 1) ^ 1;
+    ld.len = un.len;
+    if (more) {
+      ld.look_up(a, un.i, rank);
+      if constexpr (Q4) {
+        ld.fetch_k(a, un.head, rank);
+        ld.fetch_v(a, un.head, rank);
+      }
+    }
+    while (more) {
+      const int st = n % kStages, t = rank + it * splits, head = un.head;
+      const uint32_t free_parity = ((n / kStages) & 1) ^ 1;
+      const uint32_t ks = sbase + L::k0 + st * L::k_stage, vs = sbase + L::v0 + st * L::v_stage;
+      ++n;
+      // the tile behind this one, of this unit or the next with tiles
+      int nt = t + splits;
+      if (++it == mine) {
+        it = 0;
+        nt = rank;
+        do {
+          more = walk.next(a, un);
+          mine = more ? tiles_of(un) : 0;
+        } while (more && mine == 0);
+      }
       if (!__all_sync(0xffffffffu, wait(&bar.k_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
-      if (it + 1 < mine) ld.look_up(a, i, next);
-      ld.store_k(sbase + L::k0 + st * L::k_stage);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.k_full[st]);
-      if (it + 1 < mine) ld.fetch_k(a, head, next);
-      if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
-      ld.store_v(sbase + L::v0 + st * L::v_stage);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.v_full[st]);
-      if (it + 1 < mine) ld.fetch_v(a, head, next);
+      if constexpr (Q4) {
+        ld.store_k(ks);
+        if (more) {
+          ld.len = un.len;
+          ld.look_up(a, un.i, nt);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.k_full[st]);
+        if (more) ld.fetch_k(a, un.head, nt);
+        if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
+        ld.store_v(vs);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_full[st]);
+        if (more) ld.fetch_v(a, un.head, nt);
+      } else {
+        ld.copy_k(a, head, t, ks);
+        ld.fetch_v(a, head, t);
+        if (more) {
+          ld.len = un.len;
+          ld.look_up(a, un.i, nt);
+        }
+        cp_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.k_full[st]);
+        if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
+        ld.store_v(vs);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_full[st]);
+      }
     }
-  } else if (lane == 0) {
-    // --- products -----------------------------------------------------------------
+  } else {
+    // --- products: one lane issues them ---------------------------------------------
     const uint32_t id_s = idesc_f16_m128(kKeys), id_o = idesc_f16_m128(D);
-    auto issue_s = [&](int m, int st) {
+    auto issue_s = [&](int m, int st, bool last) {
+      const uint64_t q_desc = sw128_kmajor_desc(sbase + m * L::q_tile);
+      const uint64_t k_desc = sw128_kmajor_desc(sbase + L::k0 + st * L::k_stage);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        mma_f16_ss(tmem + m * 128, sw128_kmajor_desc(sbase + m * L::q_tile + off),
-                   sw128_kmajor_desc(sbase + L::k0 + st * L::k_stage + off), id_s, kk > 0);
+        const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;  // (addresses are in units of 16 bytes)
+        mma_f16_ss(tmem + m * 128, q_desc + off, k_desc + off, id_s, kk > 0);
       }
       mma_commit(&bar.s_full[m]);
+      if (last) mma_commit(&bar.k_empty[st]);
     };
-    bool ok = wait(&bar.q_full, 0, DEV_TIMEOUT_MMA);
-    if (ok && mine > 0) {
-      ok = wait(&bar.k_full[0], 0, DEV_TIMEOUT_MMA);
-      if (ok) {
-        tc_fence_after();
-        for (int m = 0; m < mtiles; ++m) issue_s(m, 0);
-        mma_commit(&bar.k_empty[0]);
-      }
-    }
-    for (int it = 0; ok && it < mine; ++it) {
-      const int st = it % kStages, ns = (it + 1) % kStages;
+    auto ready = [&](uint64_t* b, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait(b, parity, DEV_TIMEOUT_MMA)) != 0;
+    };
+    bool ok = true, more = true;
+    int n = 0;  // tiles so far
+    uint32_t q_phase = 0, p_phase = 0, o_phase = 3;  // bit m: row tile m's
+    while (ok && more) {
+      const int mtiles = un.rows > 128 ? 2 : 1, mine = tiles_of(un);
       for (int m = 0; ok && m < mtiles; ++m) {
-        if (m == 0) ok = wait(&bar.v_full[st], (it / kStages) & 1, DEV_TIMEOUT_MMA);
-        ok = ok && wait(&bar.p_full[m], it & 1, DEV_TIMEOUT_MMA);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_f16_ts(tmem + 256 + m * D, tmem + m * 128 + kk * 8,
-                     sw128_kmajor_desc(sbase + L::v0 + st * L::v_stage + (kk >> 2) * (D * 128) + (kk & 3) * 32), id_o,
-                     it > 0 || kk > 0);
-        if (m == mtiles - 1) mma_commit(&bar.v_empty[st]);
-        if (it + 1 < mine) {
-          if (m == 0) {
-            ok = wait(&bar.k_full[ns], ((it + 1) / kStages) & 1, DEV_TIMEOUT_MMA);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          issue_s(m, ns);  // over P: the products run in the order of issue
-          if (m == mtiles - 1) mma_commit(&bar.k_empty[ns]);
+        ok = ready(&bar.q_full[m], (q_phase >> m) & 1);
+        q_phase ^= 1u << m;
+        if (ok && mine > 0) {
+          if (m == 0) ok = ready(&bar.k_full[n % kStages], (n / kStages) & 1);
+          tc_fence_after();
+          if (ok && elect_one()) issue_s(m, n % kStages, m == mtiles - 1);
+          __syncwarp();
         }
       }
+      for (int it = 0; ok && it < mine; ++it, ++n) {
+        const int st = n % kStages, ns = (n + 1) % kStages;
+        for (int m = 0; m < mtiles; ++m) {
+          if (m == 0) ok = ready(&bar.v_full[st], (n / kStages) & 1);
+          if (it == 0) {  // the last unit's output has been read
+            ok = ok && ready(&bar.o_free[m], (o_phase >> m) & 1);
+            o_phase ^= 1u << m;
+          }
+          ok = ok && ready(&bar.p_full[m], (p_phase >> m) & 1);
+          p_phase ^= 1u << m;
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t v_desc = sw128_kmajor_desc(sbase + L::v0 + st * L::v_stage);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_f16_ts(tmem + 256 + m * D, tmem + m * 128 + kk * 8,
+                         v_desc + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4), id_o, it > 0 || kk > 0);
+            if (it + 1 == mine) mma_commit(&bar.o_full[m]);
+            if (m == mtiles - 1) mma_commit(&bar.v_empty[st]);
+          }
+          __syncwarp();
+          if (it + 1 < mine) {
+            if (m == 0) ok = ready(&bar.k_full[ns], ((n + 1) / kStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) issue_s(m, ns, m == mtiles - 1);  // over P: the products run in the order of issue
+            __syncwarp();
+          }
+        }
+      }
+      if (ok && mine == 0 && elect_one())  // a share of no tiles (of a cluster's unit): nothing to add
+        for (int m = 0; m < mtiles; ++m) mma_commit(&bar.o_full[m]);
+      __syncwarp();
+      if (ok) more = walk.next(a, un);
     }
-    mma_commit(&bar.done);
-    // the products in flight have read shared and tensor memory before the CTA lets go of
-    // them, whatever the waits' limit
-    if (!mbar_wait(&bar.done, 0, kDrainNs)) set_error(a.err, DEV_TIMEOUT_MMA);
+    __syncwarp();
+    if (elect_one()) {
+      mma_commit(&bar.done);
+      // the products in flight have read shared and tensor memory before the CTA lets go of
+      // them, whatever the waits' limit
+      if (!mbar_wait(&bar.done, 0, kDrainNs)) set_error(a.err, DEV_TIMEOUT_MMA);
+    }
   }
   __syncwarp();
   tc_fence_before();
@@ -582,6 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   bool fine = true;
   for (int k = 0; k < splits; ++k) fine &= *cluster.map_shared_rank(&s_fail, k) == 0;
   constexpr int C4 = D / 4;
+  walk.start(a, blockIdx.x / splits, gridDim.x / splits);  // the cluster's one unit again
+  walk.next(a, un);
+  const int rows = un.rows;
   // (an aligned base is at the same offset in every CTA of the launch)
   const float4* parts = reinterpret_cast<const float4*>(smem + L::k0);
   for (int x = rank * kThreads + threadIdx.x; fine && x < rows * C4; x += splits * kThreads) {
@@ -609,8 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         acc.w += f * pk[k].w;
       }
     const float inv = 1.f / den;
-    const int c = c0 + row;
-    __half* dst = a.out + static_cast<size_t>(sp.row0 + c / g) * a.ldo + (head * g + c % g) * D;
+    const int c = un.c0 + row;
+    __half* dst = a.out + static_cast<size_t>(un.row0 + c / g) * a.ldo + (un.head * g + c % g) * D;
     const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -635,7 +845,7 @@ cudaError_t launch_d(const ChunkArgs& a, cudaStream_t s) {
   int splits = 1;
   while (splits < kMaxCluster && full * splits * 2 <= sms && a.batch.max_len > splits * 2 * 2 * kKeys) splits *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(works * splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? works * splits : std::min<long long>(works, sms)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Layout<D>::smem;
   cfg.stream = s;
