@@ -8,12 +8,13 @@
 //   O_m += P_m V   (P in tensor memory, over S; V^T in shared memory),
 // so 2 x 4 * 128 * 128 * d flops stand against one pass over the tile's codes.  Roles:
 //   warps 0-3, 4-7   softmax of row tile 0, 1: a thread owns a row (a TMEM lane), so the
-//                    running maximum and sum need no exchange.  The maximum used as
-//                    exponent base only moves when a row outgrows it by 2^8: P then stays
-//                    below 2^8 in fp16 (a relative rounding, so the base does not
-//                    matter), and O is rescaled rarely;
-//   warps 8-11       bring K and V: pages looked up, codes fetched a tile ahead
-//                    into registers, dequantized (rounded once to fp16, as the codec's
+//                    running maximum and sum need no exchange.  The exponent base is a whole
+//                    power of two that only moves when a score outgrows it by 2^8: P then
+//                    stays below 2^8 in fp16 (a relative rounding, so the base does not
+//                    matter), a tile's scores are read once, 32 columns at a time, and where the
+//                    base moves, the factor for O and for the P already stored is exact;
+//   warps 8-15       bring K and V: pages looked up two tiles ahead, codes fetched one
+//                    tile ahead into registers, dequantized (rounded once to fp16, as the codec's
 //                    values) and stored in the 128-byte-swizzled layout; a
 //                    word of codes is one 16-byte store, since the orders of the head's
 //                    dimensions in Q K^T, of the keys in P V and of O's columns are
@@ -21,7 +22,7 @@
 //                    loaded, keys y, y + 4 of a block lie side by side, and O's columns
 //                    are unscrambled when they are stored.  V of an fp16 cache is
 //                    transposed 8 x 8 in registers;
-//   warp 12          issues the products, row tile 0's and row tile 1's by turns: while
+//   warp 16          issues the products, row tile 0's and row tile 1's by turns: while
 //                    one is in its softmax, the other's run.
 // One CTA an SM walks the units (256 query rows of a sequence and key/value head) that fall to it:
 // every role runs on into the next unit on its own, so the stores of one unit overlap the
@@ -46,9 +47,13 @@ constexpr int kRowShift = 8;  // 256 query rows of a unit
 constexpr int kRows = 1 << kRowShift;
 constexpr int kKeys = 128;
 constexpr int kStages = 2;
-constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kThreads = (kMmaWarp + 4) * 32;  // whole warpgroups, which share a register count
+// Registers a thread by role, out of the launch's 640 * 96.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kLoadRegs = 72, kMmaRegs = 64;
+static_assert(256 * kSoftmaxRegs + 256 * kLoadRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs,
+              "a split above the launch's registers would wait for ever");
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kDrainNs = 2000000000ull;
@@ -147,7 +152,51 @@ struct UnitWalk {
   }
 };
 
-// Load and wait in one statement, so that no use of the registers can move ahead of the wait.
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Waits for the loads issued so far; naming the registers keeps their uses behind it.
+__device__ __forceinline__ void tmem_wait_x32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_read_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Load and wait in one statement.
 __device__ __forceinline__ void tmem_read_x32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
@@ -159,27 +208,6 @@ __device__ __forceinline__ void tmem_read_x32(uint32_t taddr, uint32_t (&r)[32])
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
         "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
         "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_read_x64(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, "
-      "%40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
-      "%59, %60, %61, %62, %63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
-        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
-        "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]),
-        "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]),
-        "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]),
-        "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
 }
@@ -235,10 +263,25 @@ __device__ __forceinline__ uint4 ldg128(const void* p) { return __ldcg(reinterpr
 __device__ __forceinline__ uint32_t ldg32(const void* p) { return __ldcg(reinterpret_cast<const unsigned int*>(p)); }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
+// mbar_wait without the call: roles that differ in registers cannot share a function.
+__device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_test(b, parity)) return true;
+  if (limit_ns < 1000) return false;  // (a test's limit: the first probe decides)
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(b, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // Byte offset of 16-byte chunk c (0..7) of a row of a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t sw128(int row, int c) {
   return static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
 }
+
+// One key tile of a unit; t < 0: none.
+struct TileRef {
+  int i, head, t, len;
+};
 
 // What a loading lane holds of one tile: its part of up to two 8-token blocks.
 template <int D, bool Q4>
@@ -252,41 +295,40 @@ struct Loader<D, true> {
   static constexpr int units = D / 32;          // 16-byte units of a key
   uint4 k[NQ], v[NQ];
   uint32_t km[NQ], vm[NQ];
-  int page[NQ];
-  int warp, lane, sub, len;
+  int warp, lane, sub;
 
   __device__ __forceinline__ int block(int q) const { return (q * kLoadWarps + warp) * per_warp + lane / lanes; }
-  __device__ __forceinline__ void look_up(const ChunkArgs& a, int i, int t) {
+  __device__ __forceinline__ void look_up(const ChunkArgs& a, const TileRef& x, int (&page)[NQ]) const {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int p = t * kKeys + block(q) * 8;
-      page[q] = p < len ? page_of(a.kv, i, p, a.err) : -1;
+      const int p = x.t * kKeys + block(q) * 8;
+      page[q] = x.t >= 0 && p < x.len ? page_of(a.kv, x.i, p, a.err) : -1;
     }
   }
-  __device__ __forceinline__ void fetch_k(const ChunkArgs& a, int head, int t) {
+  __device__ __forceinline__ void fetch_k(const ChunkArgs& a, const TileRef& x, const int (&page)[NQ]) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       k[q] = make_uint4(0u, 0u, 0u, 0u);
       km[q] = 0u;
       if (page[q] < 0) continue;
-      const size_t slot = pool_slot(a.kv, page[q], head, t * kKeys + block(q) * 8);
+      const size_t slot = pool_slot(a.kv, page[q], x.head, x.t * kKeys + block(q) * 8);
       k[q] = ldg128(static_cast<const char*>(a.kv.k) + slot * (D / 2) + sub * 16);
       km[q] = ldg32(static_cast<const char*>(a.kv.k_meta) + (slot + sub / units) * (D / 64) * 4 +
                     (D == 128 ? ((sub % units) >> 1) * 4 : 0));
     }
   }
-  __device__ __forceinline__ void fetch_v(const ChunkArgs& a, int head, int t) {
+  __device__ __forceinline__ void fetch_v(const ChunkArgs& a, const TileRef& x, const int (&page)[NQ]) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       v[q] = make_uint4(0u, 0u, 0u, 0u);
       vm[q] = 0u;
       if (page[q] < 0) continue;
-      const int p = t * kKeys + block(q) * 8;
-      const size_t slot = pool_slot(a.kv, page[q], head, p);
+      const int p = x.t * kKeys + block(q) * 8;
+      const size_t slot = pool_slot(a.kv, page[q], x.head, p);
       v[q] = ldg128(static_cast<const char*>(a.kv.v) + slot * (D / 2) + sub * 16);
       // one pair a lane, in order; tokens behind the end read as zero (their
       // weights are zero, and 0 times an old NaN is not)
-      if (sub < 8 * (D / 64) && p + sub / (D / 64) < len)
+      if (sub < 8 * (D / 64) && p + sub / (D / 64) < x.len)
         vm[q] = ldg32(static_cast<const char*>(a.kv.v_meta) + slot * (D / 64) * 4 + sub * 4);
     }
   }
@@ -339,41 +381,42 @@ template <int D>
 struct Loader<D, false> {
   static constexpr int lanes = D / 8;  // lanes of a block: 16 bytes of each of its eight keys
   static constexpr int per_warp = 32 / lanes;
-  static constexpr int NQ = kKeys / 8 / (kLoadWarps * per_warp);
+  static constexpr int NQ = 1;  // (head width 64: half the warps have no block)
+  static_assert(kLoadWarps * per_warp >= kKeys / 8, "one turn of the warps covers a tile");
   uint4 v[NQ][8];
-  int page[NQ];
-  int warp, lane, sub, len;
+  int warp, lane, sub;
 
   __device__ __forceinline__ int block(int q) const { return (q * kLoadWarps + warp) * per_warp + lane / lanes; }
-  __device__ __forceinline__ void look_up(const ChunkArgs& a, int i, int t) {
+  __device__ __forceinline__ void look_up(const ChunkArgs& a, const TileRef& x, int (&page)[NQ]) const {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int p = t * kKeys + block(q) * 8;
-      page[q] = p < len ? page_of(a.kv, i, p, a.err) : -1;
+      const int p = x.t * kKeys + block(q) * 8;
+      page[q] = block(q) < kKeys / 8 && x.t >= 0 && p < x.len ? page_of(a.kv, x.i, p, a.err) : -1;
     }
   }
   // K straight into its swizzled place; rows behind the end are zeros.
-  __device__ __forceinline__ void copy_k(const ChunkArgs& a, int head, int t, uint32_t st) const {
+  __device__ __forceinline__ void copy_k(const ChunkArgs& a, const TileRef& x, const int (&page)[NQ], uint32_t st) const {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int p = t * kKeys + block(q) * 8;
-      const size_t slot = page[q] >= 0 ? pool_slot(a.kv, page[q], head, p) : 0;
+      const int p = x.t * kKeys + block(q) * 8;
+      const size_t slot = page[q] >= 0 ? pool_slot(a.kv, page[q], x.head, p) : 0;
+      if (block(q) >= kKeys / 8) continue;
 #pragma unroll
       for (int y = 0; y < 8; ++y)
         cp_async16(st + (sub >> 3) * (kKeys * 128) + sw128(block(q) * 8 + y, sub & 7),
-                   static_cast<const char*>(a.kv.k) + (slot + y) * (D * 2) + sub * 16, page[q] >= 0 && p + y < len);
+                   static_cast<const char*>(a.kv.k) + (slot + y) * (D * 2) + sub * 16, page[q] >= 0 && p + y < x.len);
     }
     cp_commit();
   }
-  __device__ __forceinline__ void fetch_v(const ChunkArgs& a, int head, int t) {
+  __device__ __forceinline__ void fetch_v(const ChunkArgs& a, const TileRef& x, const int (&page)[NQ]) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int p = t * kKeys + block(q) * 8;
-      const size_t slot = page[q] >= 0 ? pool_slot(a.kv, page[q], head, p) : 0;
+      const int p = x.t * kKeys + block(q) * 8;
+      const size_t slot = page[q] >= 0 ? pool_slot(a.kv, page[q], x.head, p) : 0;
 #pragma unroll
       for (int y = 0; y < 8; ++y) {
         v[q][y] = make_uint4(0u, 0u, 0u, 0u);
-        if (page[q] >= 0 && p + y < len)
+        if (page[q] >= 0 && p + y < x.len)
           v[q][y] = ldg128(static_cast<const char*>(a.kv.v) + (slot + y) * (D * 2) + sub * 16);
       }
     }
@@ -382,6 +425,7 @@ struct Loader<D, false> {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const int blk = block(q);
+      if (blk >= kKeys / 8) continue;
       const uint32_t base = st + (blk >> 3) * (D * 128);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -448,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   auto wait = [&](uint64_t* b, uint32_t parity, uint32_t code) {
-    if (mbar_wait(b, parity, a.limit_ns)) return true;
+    if (wait_phase(b, parity, a.limit_ns)) return true;
     set_error(a.err, code);
     atomicExch(&s_fail, 1);
     return false;
@@ -457,11 +501,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   auto tiles_of = [&](const Unit& x) { return x.tiles > rank ? (x.tiles - rank + splits - 1) / splits : 0; };
 
   if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // --- softmax of one row -------------------------------------------------------
     const int m = warp >> 2, row = threadIdx.x;  // row of the unit: TMEM lane row % 128 of row tile m
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + m * 128, o_col = tmem + lanes + 256 + m * D;
-    const float slack = 8.f / a.scale_log2;
+    const float inv_scale = 1.f / a.scale_log2;
     // Q's row into its swizzled place (every product that read the last one has completed)
     auto load_q = [&](const Unit& x) {
       const bool live = row < x.rows;
@@ -492,29 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       const int c = cur.c0 + (live ? row : 0), tok = c / g;
       const int pos = live ? cur.first + tok : cur.len;
       const int mine = tiles_of(cur);
-      float base = -INFINITY;  // exponent base, a raw score
+      float base = -INFINITY;   // exponent base: log2 of the weights' unit, a whole number
+      float limit = -INFINITY;  // the raw score that moves it
       uint64_t sum = 0;        // sums of the even and the odd columns' weights
       for (int it = 0; it < mine; ++it) {
         if (!(ok = __all_sync(0xffffffffu, wait(&bar.s_full[m], s_phase, DEV_TIMEOUT_EPILOGUE)))) break;
         s_phase ^= 1;
         tc_fence_after();
         const int lim = pos - (rank + it * splits) * kKeys;  // tokens 0 .. lim of the tile count
-        const bool masked = __any_sync(0xffffffffu, lim < kKeys - 1);
-        float top = -INFINITY;
-        if (!masked) {
-          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t s[64];
-            tmem_read_x64(s_col + 64 * h, s);
-#pragma unroll
-            for (int e = 0; e < 64; e += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                t4[k] = max3(t4[k], __uint_as_float(s[e + 2 * k]), __uint_as_float(s[e + 2 * k + 1]));
-          }
-          top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
-        } else {
+        if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
           // the scores behind the row's position leave S here
 #pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
@@ -525,49 +556,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
             for (int e = 0; e < 32; ++e) {
               const int t = Q4 ? (e & ~7) + ((e & 7) >> 1) + 4 * (e & 1) : e;
               if (t > here) s[e] = 0xff800000u;
-              top = fmaxf(top, __uint_as_float(s[e]));
             }
             tmem_st_x32(s_col + 32 * ch, s);
           }
           tmem_st_wait();
         }
-        const bool move = top > base + slack;  // (from -inf: any finite score)
-        if (__any_sync(0xffffffffu, move)) {
-          const float nb = move ? top : base;
-          const float alpha = base == -INFINITY ? 0.f : exp2_approx((base - nb) * a.scale_log2);
-          base = nb;
-          float s0, s1;
-          unpair(sum, s0, s1);
-          sum = pair(__float_as_uint(s0 * alpha), __float_as_uint(s1 * alpha));
-          if (it > 0) {
-#pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-              uint32_t o[32];
-              tmem_read_x32(o_col + 32 * ch, o);
+        uint64_t sums[4] = {sum, 0, 0, 0};
+        uint32_t s[2][32];
+        tmem_ld_x32(s_col, s[0]);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st_x32(o_col + 32 * ch, o);
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t(&x)[32] = s[ch & 1];
+          tmem_wait_x32(x);
+          if (ch < 3) tmem_ld_x32(s_col + 32 * (ch + 1), s[(ch + 1) & 1]);
+          float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            top = max3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            top1 = max3(top1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+          }
+          top = fmaxf(top, top1);
+          if (__any_sync(0xffffffffu, top > limit)) {  // (from -inf: any finite score)
+            const float nb = top > limit ? ceilf(top * a.scale_log2) : base;
+            const float alpha = base == -INFINITY ? 0.f : exp2_approx(base - nb);
+            base = nb;
+            limit = (nb + 8.f) * inv_scale;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float s0, s1;
+              unpair(sums[k], s0, s1);
+              sums[k] = pair(__float_as_uint(s0 * alpha), __float_as_uint(s1 * alpha));
+            }
+            const __half2 alpha2 = __float2half2_rn(alpha);
+#pragma unroll 1
+            for (int q = 0; q < ch; ++q) {
+              uint32_t o[16];
+              tmem_read_x16(s_col + 16 * q, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const __half2 y = __hmul2(as_half2(o[e]), alpha2);
+                o[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              tmem_st_x16(s_col + 16 * q, o);
+            }
+            if (it > 0) {
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_read_x16(o_col + 16 * q, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st_x16(o_col + 16 * q, o);
+              }
             }
           }
-        }
-        const uint32_t off = __float_as_uint(base == -INFINITY ? 0.f : -base * a.scale_log2);
-        const uint64_t off2 = pair(off, off), scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
-        uint64_t sums[4] = {sum, 0, 0, 0};
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s[64], p[32];
-          tmem_read_x64(s_col + 64 * h, s);
+          const uint32_t off = __float_as_uint(base == -INFINITY ? 0.f : -base);
+          const uint64_t off2 = pair(off, off), scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
+          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
+          for (int e = 0; e < 32; e += 2) {
             float x0, x1;
-            unpair(fma2(pair(s[e], s[e + 1]), scale2, off2), x0, x1);
+            unpair(fma2(pair(x[e], x[e + 1]), scale2, off2), x0, x1);
             x0 = exp2_approx(x0);
             x1 = exp2_approx(x1);
             sums[(e / 2) & 3] = add2(sums[(e / 2) & 3], pair(__float_as_uint(x0), __float_as_uint(x1)));
             p[e / 2] = pack_half2(x0, x1);
           }
-          // over S's columns 32 h .. 32 h + 31, which are read already
-          tmem_st_x32(s_col + 32 * h, p);
+          tmem_st_x16(s_col + 16 * ch, p);  // over columns of S that are read
         }
         sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
         tmem_st_wait();
@@ -631,150 +686,129 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       }
     }
   } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     // --- K and V ------------------------------------------------------------------
-    Loader<D, Q4> ld;
+    using Ld = Loader<D, Q4>;
+    Ld ld;
     ld.warp = warp - kSoftmaxWarps;
     ld.lane = lane;
-    ld.sub = lane % Loader<D, Q4>::lanes;
-    int n = 0;  // tiles so far
+    ld.sub = lane % Ld::lanes;
     bool more = true;
     int it = 0, mine = tiles_of(un);
-    while (more && mine == 0) {
-      more = walk.next(a, un);
-      if (more) mine = tiles_of(un);
-    }
-    ld.len = un.len;
-    if (more) {
-      ld.look_up(a, un.i, rank);
-      if constexpr (Q4) {
-        ld.fetch_k(a, un.head, rank);
-        ld.fetch_v(a, un.head, rank);
+    auto advance = [&]() {  // the CTA's next tile
+      while (more && it == mine) {
+        more = walk.next(a, un);
+        it = 0;
+        mine = more ? tiles_of(un) : 0;
       }
-    }
-    while (more) {
-      const int st = n % kStages, t = rank + it * splits, head = un.head;
+      TileRef x{un.i, un.head, -1, un.len};
+      if (more) x.t = rank + it++ * splits;
+      return x;
+    };
+    TileRef cur = advance(), next = advance();
+    int page[Ld::NQ], next_page[Ld::NQ];
+    ld.look_up(a, cur, page);
+    ld.look_up(a, next, next_page);
+    if constexpr (Q4) ld.fetch_k(a, cur, page);
+    if constexpr (Q4) ld.fetch_v(a, cur, page);
+    for (int n = 0; cur.t >= 0; ++n) {
+      const int st = n % kStages;
       const uint32_t free_parity = ((n / kStages) & 1) ^ 1;
       const uint32_t ks = sbase + L::k0 + st * L::k_stage, vs = sbase + L::v0 + st * L::v_stage;
-      ++n;
-      // the tile behind this one, of this unit or the next with tiles
-      int nt = t + splits;
-      if (++it == mine) {
-        it = 0;
-        nt = rank;
-        do {
-          more = walk.next(a, un);
-          mine = more ? tiles_of(un) : 0;
-        } while (more && mine == 0);
-      }
       if (!__all_sync(0xffffffffu, wait(&bar.k_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
       if constexpr (Q4) {
         ld.store_k(ks);
-        if (more) {
-          ld.len = un.len;
-          ld.look_up(a, un.i, nt);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.k_full[st]);
-        if (more) ld.fetch_k(a, un.head, nt);
-        if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
-        ld.store_v(vs);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_full[st]);
-        if (more) ld.fetch_v(a, un.head, nt);
       } else {
-        ld.copy_k(a, head, t, ks);
-        ld.fetch_v(a, head, t);
-        if (more) {
-          ld.len = un.len;
-          ld.look_up(a, un.i, nt);
-        }
+        ld.copy_k(a, cur, page, ks);
+        ld.fetch_v(a, cur, page);
         cp_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.k_full[st]);
-        if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
-        ld.store_v(vs);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_full[st]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.k_full[st]);
+      if constexpr (Q4) ld.fetch_k(a, next, next_page);
+      if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
+      ld.store_v(vs);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.v_full[st]);
+      if constexpr (Q4) ld.fetch_v(a, next, next_page);
+      cur = next;
+      next = advance();
+#pragma unroll
+      for (int q = 0; q < Ld::NQ; ++q) page[q] = next_page[q];
+      ld.look_up(a, next, next_page);
     }
   } else {
-    // --- products: one lane issues them ---------------------------------------------
-    const uint32_t id_s = idesc_f16_m128(kKeys), id_o = idesc_f16_m128(D);
-    auto issue_s = [&](int m, int st, bool last) {
-      const uint64_t q_desc = sw128_kmajor_desc(sbase + m * L::q_tile);
-      const uint64_t k_desc = sw128_kmajor_desc(sbase + L::k0 + st * L::k_stage);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kMmaWarp) {
+      // --- products: one lane issues them ---------------------------------------------
+      const uint32_t id_s = idesc_f16_m128(kKeys), id_o = idesc_f16_m128(D);
+      auto issue_s = [&](int m, int st, bool last) {
+        const uint64_t q_desc = sw128_kmajor_desc(sbase + m * L::q_tile);
+        const uint64_t k_desc = sw128_kmajor_desc(sbase + L::k0 + st * L::k_stage);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;  // (addresses are in units of 16 bytes)
-        mma_f16_ss(tmem + m * 128, q_desc + off, k_desc + off, id_s, kk > 0);
-      }
-      mma_commit(&bar.s_full[m]);
-      if (last) mma_commit(&bar.k_empty[st]);
-    };
-    auto ready = [&](uint64_t* b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait(b, parity, DEV_TIMEOUT_MMA)) != 0;
-    };
-    bool ok = true, more = true;
-    int n = 0;  // tiles so far
-    uint32_t q_phase = 0, p_phase = 0, o_phase = 3;  // bit m: row tile m's
-    while (ok && more) {
-      const int mtiles = un.rows > 128 ? 2 : 1, mine = tiles_of(un);
-      for (int m = 0; ok && m < mtiles; ++m) {
-        ok = ready(&bar.q_full[m], (q_phase >> m) & 1);
-        q_phase ^= 1u << m;
-        if (ok && mine > 0) {
-          if (m == 0) ok = ready(&bar.k_full[n % kStages], (n / kStages) & 1);
-          tc_fence_after();
-          if (ok && elect_one()) issue_s(m, n % kStages, m == mtiles - 1);
-          __syncwarp();
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;  // (addresses are in units of 16 bytes)
+          mma_f16_ss(tmem + m * 128, q_desc + off, k_desc + off, id_s, kk > 0);
         }
-      }
-      for (int it = 0; ok && it < mine; ++it, ++n) {
-        const int st = n % kStages, ns = (n + 1) % kStages;
-        for (int m = 0; m < mtiles; ++m) {
-          if (m == 0) ok = ready(&bar.v_full[st], (n / kStages) & 1);
-          if (it == 0) {  // the last unit's output has been read
-            ok = ok && ready(&bar.o_free[m], (o_phase >> m) & 1);
-            o_phase ^= 1u << m;
-          }
-          ok = ok && ready(&bar.p_full[m], (p_phase >> m) & 1);
-          p_phase ^= 1u << m;
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t v_desc = sw128_kmajor_desc(sbase + L::v0 + st * L::v_stage);
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_f16_ts(tmem + 256 + m * D, tmem + m * 128 + kk * 8,
-                         v_desc + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4), id_o, it > 0 || kk > 0);
-            if (it + 1 == mine) mma_commit(&bar.o_full[m]);
-            if (m == mtiles - 1) mma_commit(&bar.v_empty[st]);
-          }
-          __syncwarp();
-          if (it + 1 < mine) {
-            if (m == 0) ok = ready(&bar.k_full[ns], ((n + 1) / kStages) & 1);
-            if (!ok) break;
+        mma_commit(&bar.s_full[m]);
+        if (last) mma_commit(&bar.k_empty[st]);
+      };
+      auto ready = [&](uint64_t* b, uint32_t parity) { return wait(b, parity, DEV_TIMEOUT_MMA); };
+      bool ok = true, more = true;
+      int n0 = 0;  // tiles of the units before
+      uint32_t q_phase = 0, p_phase = 0, o_phase = 3;  // bit m: row tile m's
+      while (ok && more) {
+        const int mtiles = un.rows > 128 ? 2 : 1, mine = tiles_of(un);
+        if (elect_one()) {
+          if (mine > 0) ok = ready(&bar.k_full[n0 % kStages], (n0 / kStages) & 1);
+          for (int m = 0; ok && m < mtiles; ++m) {
+            ok = ready(&bar.q_full[m], (q_phase >> m) & 1);
             tc_fence_after();
-            if (elect_one()) issue_s(m, ns, m == mtiles - 1);  // over P: the products run in the order of issue
-            __syncwarp();
+            if (ok && mine > 0) issue_s(m, n0 % kStages, m == mtiles - 1);
+            if (ok && mine == 0) mma_commit(&bar.o_full[m]);  // a share of no tiles: nothing to add
+          }
+          uint32_t p_par = p_phase;
+          for (int it = 0; ok && it < mine; ++it, p_par ^= 3) {
+            const int n = n0 + it, st = n % kStages, ns = (n + 1) % kStages;
+            const uint64_t v_desc = sw128_kmajor_desc(sbase + L::v0 + st * L::v_stage);
+            ok = ready(&bar.v_full[st], (n / kStages) & 1);
+            for (int m = 0; ok && m < mtiles; ++m) {
+              if (it == 0) ok = ready(&bar.o_free[m], (o_phase >> m) & 1);  // the last unit's output has been read
+              ok = ok && ready(&bar.p_full[m], (p_par >> m) & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_f16_ts(tmem + 256 + m * D, tmem + m * 128 + kk * 8,
+                           v_desc + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4), id_o, it > 0 || kk > 0);
+              if (it + 1 == mine) mma_commit(&bar.o_full[m]);
+              if (m == mtiles - 1) mma_commit(&bar.v_empty[st]);
+              if (it + 1 < mine) {
+                if (m == 0) ok = ready(&bar.k_full[ns], ((n + 1) / kStages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(m, ns, m == mtiles - 1);  // over P: the products run in the order of issue
+              }
+            }
           }
         }
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        const uint32_t used = mtiles == 2 ? 3 : 1;
+        n0 += mine;
+        q_phase ^= used;
+        if (mine > 0) o_phase ^= used;
+        if (mine & 1) p_phase ^= used;
+        if (ok) more = walk.next(a, un);
       }
-      if (ok && mine == 0 && elect_one())  // a share of no tiles (of a cluster's unit): nothing to add
-        for (int m = 0; m < mtiles; ++m) mma_commit(&bar.o_full[m]);
       __syncwarp();
-      if (ok) more = walk.next(a, un);
-    }
-    __syncwarp();
-    if (elect_one()) {
-      mma_commit(&bar.done);
-      // the products in flight have read shared and tensor memory before the CTA lets go of
-      // them, whatever the waits' limit
-      if (!mbar_wait(&bar.done, 0, kDrainNs)) set_error(a.err, DEV_TIMEOUT_MMA);
+      if (elect_one()) {
+        mma_commit(&bar.done);
+        // the products in flight have read shared and tensor memory before the CTA lets go of
+        // them, whatever the waits' limit
+        if (!wait_phase(&bar.done, 0, kDrainNs)) set_error(a.err, DEV_TIMEOUT_MMA);
+      }
     }
   }
   __syncwarp();
@@ -796,28 +830,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   const float4* parts = reinterpret_cast<const float4*>(smem + L::k0);
   for (int x = rank * kThreads + threadIdx.x; fine && x < rows * C4; x += splits * kThreads) {
     const int row = x / C4, c4 = x % C4;
-    float top = -INFINITY, mk[kMaxCluster], lk[kMaxCluster];
-    float4 pk[kMaxCluster];
-#pragma unroll
-    for (int k = 0; k < kMaxCluster; ++k)
-      if (k < splits) {
-        mk[k] = *cluster.map_shared_rank(&s_m[row], k);
-        lk[k] = *cluster.map_shared_rank(&s_l[row], k);
-        pk[k] = *cluster.map_shared_rank(parts + row * C4 + (c4 ^ (row & 7)), k);
-        top = fmaxf(top, mk[k]);
-      }
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int k = 0; k < splits; ++k) top = fmaxf(top, *cluster.map_shared_rank(&s_m[row], k));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
-#pragma unroll
-    for (int k = 0; k < kMaxCluster; ++k)
-      if (k < splits && mk[k] != -INFINITY) {
-        const float f = exp2_approx((mk[k] - top) * a.scale_log2);
-        den += f * lk[k];
-        acc.x += f * pk[k].x;
-        acc.y += f * pk[k].y;
-        acc.z += f * pk[k].z;
-        acc.w += f * pk[k].w;
-      }
+#pragma unroll 1
+    for (int k = 0; k < splits; ++k) {
+      const float mk = *cluster.map_shared_rank(&s_m[row], k);
+      const float4 pk = *cluster.map_shared_rank(parts + row * C4 + (c4 ^ (row & 7)), k);
+      const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - top);
+      den += f * *cluster.map_shared_rank(&s_l[row], k);
+      acc.x += f * pk.x;
+      acc.y += f * pk.y;
+      acc.z += f * pk.z;
+      acc.w += f * pk.w;
+    }
     const float inv = 1.f / den;
     const int c = un.c0 + row;
     __half* dst = a.out + static_cast<size_t>(un.row0 + c / g) * a.ldo + (un.head * g + c % g) * D;
