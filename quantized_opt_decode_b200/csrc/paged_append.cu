@@ -1,14 +1,18 @@
 // Paged KV cache: append (position rotation, quantization and page lookup in
 // one pass) and read-back of a ragged batch of tokens.
 //
-// One warp takes one 8-token block of one sequence and one head of K, of V or
-// (rotation only) of Q.  The 8-token block is the unit in which the 4-bit V
-// codes are interleaved, so the warp owns the words it writes: a block that the
-// new tokens cover only in part is read, merged and written back without atomics,
-// and slots before and behind the new tokens keep their codes.  A lane holds d/32
-// neighbouring dimensions of up to 8 tokens, so a 64-element group is 16 (d =
-// 128) or 32 (d = 64) lanes and its min and max are one shuffle ladder on the pair
-// (min x, -max x) in two fp16 halves.
+// A warp takes one 8-token block of one sequence and a few neighbouring heads of K,
+// of V or (rotation only) of Q.  The 8-token block is the unit in which the 4-bit V codes are
+// interleaved, so the warp owns the words it writes: a block that the new tokens
+// cover only in part is read, merged and written back without atomics, and slots before
+// and behind the new tokens keep their codes.  A lane holds 16 dimensions of one head as
+// two 16-byte chunks: the two halves of its rotation pairs, so that no value is loaded
+// twice and a token's cosines and sines (64 bytes a lane) serve all the heads of the warp; past the
+// rotated dimensions, and in V, 16 neighbouring ones.  A 64-element group is then
+// spread over the 8 (d = 128) or 4 lanes of the head: its minimum and maximum are one
+// shuffle ladder a group on the pair (min x, -max x) in two fp16 halves.
+//
+// Memory bounds both kernels: rows in, codes and pairs out, and for Q rows in and out.
 //
 // The codes are exactly those of flexq_quantize on the (rotated) fp16 rows:
 // rotation multiplies and adds in fp32 without contraction and rounds once to
@@ -23,35 +27,147 @@ constexpr int kWarps = 8;
 constexpr int kUnitShift = 3;  // units of 8 tokens
 constexpr int kUnitExtra = 2;  // n tokens at any phase touch at most floor(n / 8) + 2 blocks
 
-template <int VEC>
-struct Vec;
-template <>
-struct Vec<4> {
-  using T = uint2;
-};
-template <>
-struct Vec<2> {
-  using T = uint32_t;
-};
+constexpr int kQHeads = 4;       // heads of Q that a lane takes in turn
 
-template <int VEC>
-__device__ __forceinline__ void unpack(const typename Vec<VEC>::T& raw, float (&x)[VEC]) {
+// Elements of a 16-byte chunk.
+__device__ __forceinline__ void unpack(const uint4& raw, float (&x)[8]) {
   const __half2* h = reinterpret_cast<const __half2*>(&raw);
 #pragma unroll
-  for (int e = 0; e < VEC / 2; ++e) {
+  for (int e = 0; e < 4; ++e) {
     const float2 f = __half22float2(h[e]);
     x[2 * e] = f.x;
     x[2 * e + 1] = f.y;
   }
 }
-
-template <int VEC>
-__device__ __forceinline__ typename Vec<VEC>::T pack16(const float (&x)[VEC]) {
-  typename Vec<VEC>::T raw;
+__device__ __forceinline__ uint4 pack16(const float (&x)[8]) {
+  uint4 raw;
   __half2* h = reinterpret_cast<__half2*>(&raw);
 #pragma unroll
-  for (int e = 0; e < VEC / 2; ++e) h[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+  for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
   return raw;
+}
+
+// The two chunks of lane p of a head: dimensions ea .. ea + 7 and eb .. eb + 7.
+struct Slot {
+  int ea, eb;
+  bool turned;
+};
+__device__ __forceinline__ Slot slot_of(int p, int rot, bool interleaved) {
+  Slot s;
+  s.turned = p < rot / 16;
+  s.ea = s.turned && !interleaved ? 8 * p : 16 * p;
+  s.eb = s.turned && !interleaved ? rot / 2 + 8 * p : 16 * p + 8;
+  return s;
+}
+
+// Cosines and sines of the lane's eight pairs at position pos.
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_turn(const RopeView& rope, int pos, int p, Turn& t) {
+  const float* row = rope.cos_sin + static_cast<size_t>(pos) * rope.rot_dim + 8 * p;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    *reinterpret_cast<float4*>(&t.c[4 * h]) = __ldg(reinterpret_cast<const float4*>(row) + h);
+    *reinterpret_cast<float4*>(&t.s[4 * h]) = __ldg(reinterpret_cast<const float4*>(row + rope.rot_dim / 2) + h);
+  }
+}
+
+// a' = a cos - b sin, b' = b cos + a sin, every operation rounded.
+__device__ __forceinline__ void turn_chunks(uint4& ra, uint4& rb, const Turn& t, bool interleaved) {
+  float x[8], y[8], u[8], v[8];
+  unpack(ra, x);
+  unpack(rb, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // pair i: (x[i], y[i]), or elements 2i and 2i + 1 of the 16
+    const float a = interleaved ? (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]) : x[i];
+    const float b = interleaved ? (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]) : y[i];
+    u[i] = __fsub_rn(__fmul_rn(a, t.c[i]), __fmul_rn(b, t.s[i]));
+    v[i] = __fadd_rn(__fmul_rn(b, t.c[i]), __fmul_rn(a, t.s[i]));
+  }
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = u[i];
+      x[2 * i + 1] = v[i];
+      y[2 * i] = u[4 + i];
+      y[2 * i + 1] = v[4 + i];
+    }
+    ra = pack16(x);
+    rb = pack16(y);
+  } else {
+    ra = pack16(u);
+    rb = pack16(v);
+  }
+}
+
+// (min, -max) of a chunk as two fp16 halves.
+__device__ __forceinline__ uint32_t chunk_range(const uint4& raw) {
+  const __half2* h = reinterpret_cast<const __half2*>(&raw);
+  const __half2 lo = __hmin2(__hmin2(h[0], h[1]), __hmin2(h[2], h[3]));
+  const __half2 hi = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  const __half l = __hmin(__low2half(lo), __high2half(lo)), m = __hmax(__low2half(hi), __high2half(hi));
+  return __half_as_ushort(l) | (static_cast<uint32_t>(__half_as_ushort(m) ^ 0x8000u) << 16);
+}
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y) {
+  const __half2 m = __hmin2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+struct Group {
+  __half2 pair;  // (min, scale) as stored
+  float mn, sc, inv;
+};
+__device__ __forceinline__ Group group_of(uint32_t range) {
+  const float lo = __fadd_rn(__half2float(__ushort_as_half(range & 0xffffu)), 0.0f);  // -0 -> +0
+  const float hi = __fadd_rn(__half2float(__ushort_as_half((range >> 16) ^ 0x8000u)), 0.0f);
+  const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+  const __half m16 = __float2half_rn(lo);
+  Group g;
+  g.pair = __halves2half2(m16, s16);
+  g.mn = __half2float(m16);
+  g.sc = __half2float(s16);
+  g.inv = g.sc != 0.0f ? __frcp_rn(g.sc) : 0.0f;
+  return g;
+}
+
+// Codes of a chunk.
+__device__ __forceinline__ void chunk_codes(const uint4& raw, const Group& g, uint32_t (&c)[8]) {
+  float x[8];
+  unpack(raw, x);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c[e] = g.sc != 0.0f ? q64_code(__fsub_rn(x[e], g.mn), g.sc, g.inv) : 0u;
+}
+
+// The lane's two chunks quantized with their head's groups; every lane of the warp
+// calls this.  The lane p < d/64 of a head stores the pair of group p.
+template <int D>
+__device__ __forceinline__ void quantize(const uint4& ra, const uint4& rb, const Slot& s, int p, bool live, __half2* meta,
+                                         uint32_t (&ca)[8], uint32_t (&cb)[8]) {
+  uint32_t a = chunk_range(ra), b = chunk_range(rb);
+  if (D == 64) {
+    a = min2(a, b);
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) a = min2(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const Group g = group_of(a);
+    if (p == 0 && live) meta[0] = g.pair;
+    chunk_codes(ra, g, ca);
+    chunk_codes(rb, g, cb);
+  } else {
+    constexpr uint32_t kNone = 0x7c007c00u;  // (inf, inf)
+    uint32_t r0 = min2(s.ea < 64 ? a : kNone, s.eb < 64 ? b : kNone);
+    uint32_t r1 = min2(s.ea < 64 ? kNone : a, s.eb < 64 ? kNone : b);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      r0 = min2(r0, __shfl_xor_sync(0xffffffffu, r0, o));
+      r1 = min2(r1, __shfl_xor_sync(0xffffffffu, r1, o));
+    }
+    const Group ga = group_of(s.ea < 64 ? r0 : r1), gb = group_of(s.eb < 64 ? r0 : r1);
+    if (p < 2 && live) meta[p] = group_of(p == 0 ? r0 : r1).pair;
+    chunk_codes(ra, ga, ca);
+    chunk_codes(rb, gb, cb);
+  }
 }
 
 // A unit's sequence and block: tokens t0 .. t1-1 (positions) of sequence i.
@@ -93,174 +209,147 @@ struct AppendArgs {
   int ldq;
   __half* q_out;
   int ldqo;
-  int jobs;  // K heads, V heads, Q heads of a unit
+  int kv_jobs, jobs;  // of a block: K's (and V's), and all with Q's
   long long total;
   uint32_t* err;
 };
 
+// kind of a job: K, V or Q of a block and a warp's heads
+enum Kind { kK, kV, kQ };
+
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendArgs a) {
-  constexpr int VEC = D / 32;
-  using V = typename Vec<VEC>::T;
+  constexpr int LH = D / 16;     // lanes of a head
+  constexpr int HW = 32 / LH;    // heads of a warp at once
+  constexpr int G = D / 64;
   pdl_wait();
   const long long widx = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (widx >= a.total) return;
   const int lane = static_cast<int>(lane_id());
   Unit un;
   if (!find_unit(a.batch, static_cast<int>(widx / a.jobs), un, a.err)) return;
-  const int job = static_cast<int>(widx % a.jobs);
+  int job = static_cast<int>(widx % a.jobs);
   const int kvh = a.kv.kv_heads;
-  const bool is_k = job < kvh, is_v = !is_k && job < 2 * kvh, is_q = !is_k && !is_v;
-  const int head = is_k ? job : (is_v ? job - kvh : job - 2 * kvh);
-  const __half* src = is_k ? a.k : (is_v ? a.v : a.q);
-  const int lds = is_q ? a.ldq : a.ld;
-  const int e0 = lane * VEC;
-  const int base = un.t0 & ~7;
+  const Kind kind = job < a.kv_jobs ? kK : job < 2 * a.kv_jobs ? kV : kQ;
+  job -= kind * a.kv_jobs;
+  const int p = lane % LH;
+  const bool turn = a.rope.cos_sin != nullptr && kind != kV;
+  const bool inter = a.rope.interleaved != 0;
+  if (turn && un.t1 > a.rope.max_pos) {
+    if (lane == 0) set_error(a.err, DEV_BAD_ARGUMENT);
+    return;
+  }
+  const Slot sl = slot_of(p, turn ? a.rope.rot_dim : 0, inter);
 
-  // the lane's dimensions of the block's tokens, all loads in flight at once
-  V raw[8];
+  if (kind == kQ) {
+    const int h0 = job * HW * kQHeads + lane / LH;
+    for (int t = un.t0; t < un.t1; ++t) {
+      const size_t row = static_cast<size_t>(un.row + t);
+      uint4 ra[kQHeads], rb[kQHeads];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    const int p = base + t;
-    raw[t] = V{};
-    if (p >= un.t0 && p < un.t1)
-      raw[t] = *reinterpret_cast<const V*>(src + static_cast<size_t>(un.row + p) * lds + head * D + e0);
-  }
-  if (a.rope.cos_sin != nullptr && !is_v) {
-    if (un.t1 > a.rope.max_pos) {
-      if (lane == 0) set_error(a.err, DEV_BAD_ARGUMENT);
-      return;
-    }
-    const int rot = a.rope.rot_dim, half_rot = rot / 2;
-    const bool turned = e0 < rot;
-    const bool upper = !a.rope.interleaved && e0 >= half_rot;  // the lane holds the pairs' second elements
-    if (turned) {
-      V other[8];
-      if (!a.rope.interleaved) {
-        const int eo = upper ? e0 - half_rot : e0 + half_rot;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const int p = base + t;
-          other[t] = V{};
-          if (p >= un.t0 && p < un.t1)
-            other[t] = *reinterpret_cast<const V*>(src + static_cast<size_t>(un.row + p) * lds + head * D + eo);
-        }
+      for (int i = 0; i < kQHeads; ++i) {
+        const int h = h0 + i * HW;
+        if (h >= a.heads) continue;
+        const __half* src = a.q + row * a.ldq + h * D;
+        ra[i] = *reinterpret_cast<const uint4*>(src + sl.ea);
+        rb[i] = *reinterpret_cast<const uint4*>(src + sl.eb);
       }
+      if (sl.turned) {
+        Turn tn;
+        load_turn(a.rope, t, p, tn);
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const int p = base + t;
-        if (p < un.t0 || p >= un.t1) continue;
-        const float* cs = a.rope.cos_sin + static_cast<size_t>(p) * rot;
-        float x[VEC], y[VEC];
-        unpack<VEC>(raw[t], x);
-        if (a.rope.interleaved) {
-#pragma unroll
-          for (int e = 0; e < VEC; e += 2) {
-            const float c = cs[(e0 + e) / 2], s = cs[half_rot + (e0 + e) / 2];
-            y[e] = __fsub_rn(__fmul_rn(x[e], c), __fmul_rn(x[e + 1], s));
-            y[e + 1] = __fadd_rn(__fmul_rn(x[e + 1], c), __fmul_rn(x[e], s));
-          }
-        } else {
-          float z[VEC];
-          unpack<VEC>(other[t], z);
-          const int a0 = upper ? e0 - half_rot : e0;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float c = cs[a0 + e], s = cs[half_rot + a0 + e];
-            const float xs = __fmul_rn(z[e], s);
-            y[e] = upper ? __fadd_rn(__fmul_rn(x[e], c), xs) : __fsub_rn(__fmul_rn(x[e], c), xs);
-          }
-        }
-        raw[t] = pack16<VEC>(y);
+        for (int i = 0; i < kQHeads; ++i) turn_chunks(ra[i], rb[i], tn, inter);
       }
-    }
-    __syncwarp();  // in place: every lane has read its pairs before any lane writes
-  }
-  if (is_q) {
+      // (in place: a lane writes the chunks that it alone has read)
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int p = base + t;
-      if (p >= un.t0 && p < un.t1)
-        *reinterpret_cast<V*>(a.q_out + static_cast<size_t>(un.row + p) * a.ldqo + head * D + e0) = raw[t];
+      for (int i = 0; i < kQHeads; ++i) {
+        const int h = h0 + i * HW;
+        if (h >= a.heads) continue;
+        __half* dst = a.q_out + row * a.ldqo + h * D;
+        *reinterpret_cast<uint4*>(dst + sl.ea) = ra[i];
+        *reinterpret_cast<uint4*>(dst + sl.eb) = rb[i];
+      }
     }
     return;
   }
+
+  const int head = job * HW + lane / LH;
+  const bool live = head < kvh;
+  const int base = un.t0 & ~7;
   const int page = page_of(a.kv, un.i, base, a.err);
   if (page < 0) return;
-  const size_t slot0 = pool_slot(a.kv, page, head, base);
-  if (!Q4) {
-    __half* dst = static_cast<__half*>(is_k ? a.kv.k : a.kv.v);
+  const size_t slot0 = pool_slot(a.kv, page, live ? head : 0, base);
+  const __half* src = (kind == kK ? a.k : a.v) + (live ? head : 0) * D;
+  // V's words of 16 dimensions: kept where the new tokens cover the block only in part
+  uint32_t w[16];
+  uint4* words = reinterpret_cast<uint4*>(static_cast<uint32_t*>(a.kv.v) + (slot0 >> 3) * D + 16 * p);
+  if (Q4 && kind == kV) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int p = base + t;
-      if (p >= un.t0 && p < un.t1) *reinterpret_cast<V*>(dst + (slot0 + t) * D + e0) = raw[t];
-    }
-    return;
-  }
-  constexpr int G = D / 64;
-  constexpr int kGroupLanes = 64 / VEC;
-  uint32_t* words = static_cast<uint32_t*>(a.kv.v) + (slot0 >> 3) * D + e0;
-  const bool whole = un.t1 - un.t0 == 8;
-  uint32_t w[VEC];
+    for (int e = 0; e < 16; ++e) w[e] = 0u;
+    if (un.t1 - un.t0 < 8) {
+      uint32_t kept = 0xffffffffu;
+      kept &= ~(((1ull << (4 * (un.t1 - un.t0))) - 1) << (4 * (un.t0 - base)));
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) w[e] = 0u;
-  if (is_v && !whole) {
-    uint32_t kept = 0xffffffffu;
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if (base + t >= un.t0 && base + t < un.t1) kept &= ~(0xFu << (4 * t));
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) w[e] = words[e] & kept;
-  }
-  __half2* meta = static_cast<__half2*>(is_k ? a.kv.k_meta : a.kv.v_meta);
-#pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    const int p = base + t;
-    if (p < un.t0 || p >= un.t1) continue;
-    float x[VEC];
-    unpack<VEC>(raw[t], x);
-    const __half2* h = reinterpret_cast<const __half2*>(&raw[t]);
-    // (min x, -max x) of the lane's values, then of the group
-    __half2 lo2 = h[0], hi2 = h[0];
-    if (VEC == 4) {
-      lo2 = __hmin2(lo2, h[VEC / 2 - 1]);
-      hi2 = __hmax2(hi2, h[VEC / 2 - 1]);
-    }
-    const __half lo1 = __hmin(__low2half(lo2), __high2half(lo2)), hi1 = __hmax(__low2half(hi2), __high2half(hi2));
-    uint32_t mm = __half_as_ushort(lo1) | (static_cast<uint32_t>(__half_as_ushort(hi1) ^ 0x8000u) << 16);
-#pragma unroll
-    for (int o = kGroupLanes / 2; o > 0; o >>= 1) {
-      const uint32_t r = __shfl_xor_sync(0xffffffffu, mm, o);
-      const __half2 m2 = __hmin2(*reinterpret_cast<const __half2*>(&mm), *reinterpret_cast<const __half2*>(&r));
-      mm = *reinterpret_cast<const uint32_t*>(&m2);
-    }
-    const float lo = __fadd_rn(__half2float(__ushort_as_half(mm & 0xffffu)), 0.0f);  // -0 -> +0
-    const float hi = __fadd_rn(__half2float(__ushort_as_half((mm >> 16) ^ 0x8000u)), 0.0f);
-    const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-    const __half m16 = __float2half_rn(lo);
-    const float sc = __half2float(s16), mn = __half2float(m16);
-    const float inv = sc != 0.0f ? __frcp_rn(sc) : 0.0f;
-    uint32_t c[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) c[e] = sc != 0.0f ? q64_code(__fsub_rn(x[e], mn), sc, inv) : 0u;
-    if (lane % kGroupLanes == 0) meta[(slot0 + t) * G + lane / kGroupLanes] = __halves2half2(m16, s16);
-    if (is_k) {
-      uint8_t* dst = static_cast<uint8_t*>(a.kv.k) + (slot0 + t) * (D / 2) + e0 / 2;
-      if (VEC == 4)
-        *reinterpret_cast<uint16_t*>(dst) =
-            static_cast<uint16_t>(c[0] | (c[1] << 4) | (c[VEC - 2] << 8) | (c[VEC - 1] << 12));
-      else
-        *dst = static_cast<uint8_t>(c[0] | (c[1] << 4));
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] |= c[e] << (4 * t);
+      for (int q = 0; q < 4; ++q) {
+        const uint4 old = words[q];
+        w[4 * q] = old.x & kept;
+        w[4 * q + 1] = old.y & kept;
+        w[4 * q + 2] = old.z & kept;
+        w[4 * q + 3] = old.w & kept;
+      }
     }
   }
-  if (is_v) {
-    if (VEC == 4)
-      *reinterpret_cast<uint4*>(words) = make_uint4(w[0], w[1], w[VEC - 2], w[VEC - 1]);
-    else
-      *reinterpret_cast<uint2*>(words) = make_uint2(w[0], w[1]);
+  constexpr int B = 2;  // tokens in flight
+  for (int t = un.t0; t < un.t1; t += B) {
+    uint4 ra[B], rb[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const __half* row = src + static_cast<size_t>(un.row + min(t + i, un.t1 - 1)) * a.ld;
+      ra[i] = *reinterpret_cast<const uint4*>(row + sl.ea);
+      rb[i] = *reinterpret_cast<const uint4*>(row + sl.eb);
+    }
+    if (sl.turned) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        Turn tn;
+        load_turn(a.rope, min(t + i, un.t1 - 1), p, tn);
+        turn_chunks(ra[i], rb[i], tn, inter);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (t + i >= un.t1) break;
+      const size_t slot = slot0 + (t + i - base);
+      if (!Q4) {
+        __half* dst = static_cast<__half*>(kind == kK ? a.kv.k : a.kv.v) + slot * D;
+        if (live) {
+          *reinterpret_cast<uint4*>(dst + sl.ea) = ra[i];
+          *reinterpret_cast<uint4*>(dst + sl.eb) = rb[i];
+        }
+        continue;
+      }
+      uint32_t ca[8], cb[8];
+      __half2* meta = static_cast<__half2*>(kind == kK ? a.kv.k_meta : a.kv.v_meta) + slot * G;
+      quantize<D>(ra[i], rb[i], sl, p, live, meta, ca, cb);
+      if (kind == kK) {
+        if (live) {
+          uint8_t* dst = static_cast<uint8_t*>(a.kv.k) + slot * (D / 2);
+          *reinterpret_cast<uint32_t*>(dst + sl.ea / 2) = pack_canonical(ca);
+          *reinterpret_cast<uint32_t*>(dst + sl.eb / 2) = pack_canonical(cb);
+        }
+      } else {
+        const int sh = 4 * (t + i - base);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[e] |= ca[e] << sh;
+          w[8 + e] |= cb[e] << sh;
+        }
+      }
+    }
+  }
+  if (Q4 && kind == kV && live) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) words[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   }
 }
 
@@ -269,81 +358,96 @@ struct ReadArgs {
   RaggedView batch;
   __half *k_out, *v_out;
   int ld;
+  int kv_jobs;
   long long total;
   uint32_t* err;
 };
 
+// Eight codes of a word (element e in nibble e) as the codec's fp16 values: the
+// product with the scale is exact in fp32, so one multiply-add rounds as the codec's two
+// operations do.  (c | 0x4B000000) is the fp32 value 2^23 + c.
+__device__ __forceinline__ uint4 dequant_chunk(const uint32_t (&c)[8], float2 ms) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = fmaf(__uint_as_float(c[e] | 0x4B000000u) - 8388608.0f, ms.y, ms.x);
+  return pack16(x);
+}
+
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kWarps * 32) paged_read_kernel(const ReadArgs a) {
-  constexpr int VEC = D / 32;
-  using V = typename Vec<VEC>::T;
+  constexpr int LH = D / 16, HW = 32 / LH, G = D / 64;
   pdl_wait();
   const long long widx = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (widx >= a.total) return;
   const int lane = static_cast<int>(lane_id());
-  const int kvh = a.kv.kv_heads;
+  const int jobs = 2 * a.kv_jobs;
   Unit un;
-  if (!find_unit(a.batch, static_cast<int>(widx / (2 * kvh)), un, a.err)) return;
-  const int job = static_cast<int>(widx % (2 * kvh));
-  const bool is_k = job < kvh;
-  const int head = is_k ? job : job - kvh;
-  const int e0 = lane * VEC;
+  if (!find_unit(a.batch, static_cast<int>(widx / jobs), un, a.err)) return;
+  int job = static_cast<int>(widx % jobs);
+  const bool is_k = job < a.kv_jobs;
+  if (!is_k) job -= a.kv_jobs;
+  const int p = lane % LH, head = job * HW + lane / LH;
   const int base = un.t0 & ~7;
   const int page = page_of(a.kv, un.i, base, a.err);
-  if (page < 0) return;
+  if (page < 0 || head >= a.kv.kv_heads) return;
   const size_t slot0 = pool_slot(a.kv, page, head, base);
-  V val[8];
-  if (!Q4) {
-    const __half* src = static_cast<const __half*>(is_k ? a.kv.k : a.kv.v);
+  const int first = un.t0 - base, last = un.t1 - base;
+  __half* dst = (is_k ? a.k_out : a.v_out) + static_cast<long long>(un.row + base) * a.ld + head * D + 16 * p;
+  uint4 w[4];     // V: the block's words of 16 dimensions
+  uint2 code[8];  // K: 16 codes of each token
+  uint32_t ms[8];
+  if (Q4) {
+    const char* meta = static_cast<const char*>(is_k ? a.kv.k_meta : a.kv.v_meta) + (slot0 * G + p / 4) * 4;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int p = base + t;
-      val[t] = V{};
-      if (p >= un.t0 && p < un.t1) val[t] = *reinterpret_cast<const V*>(src + (slot0 + t) * D + e0);
-    }
-  } else {
-    constexpr int G = D / 64;
-    const __half2* meta = static_cast<const __half2*>(is_k ? a.kv.k_meta : a.kv.v_meta) + slot0 * G + e0 / 64;
-    uint32_t code[8];  // K: token t's VEC codes
-    uint32_t w[VEC];   // V: 8 tokens' codes per dimension
-    __half2 ms[8];
+    for (int t = 0; t < 8; ++t)
+      if (t >= first && t < last) ms[t] = __ldcg(reinterpret_cast<const unsigned int*>(meta + t * G * 4));
+    if (is_k) {
+      const char* src = static_cast<const char*>(a.kv.k) + slot0 * (D / 2) + 8 * p;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int p = base + t;
-      ms[t] = __half2{};
-      code[t] = 0u;
-      if (p < un.t0 || p >= un.t1) continue;
-      ms[t] = meta[t * G];
-      if (is_k) {
-        const uint8_t* src = static_cast<const uint8_t*>(a.kv.k) + (slot0 + t) * (D / 2) + e0 / 2;
-        code[t] = VEC == 4 ? *reinterpret_cast<const uint16_t*>(src) : *src;
-      }
-    }
-    if (!is_k) {
-      const uint32_t* src = static_cast<const uint32_t*>(a.kv.v) + (slot0 >> 3) * D + e0;
+      for (int t = 0; t < 8; ++t)
+        if (t >= first && t < last) code[t] = __ldcg(reinterpret_cast<const uint2*>(src + t * (D / 2)));
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(a.kv.v) + (slot0 >> 3) * D + 16 * p);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = src[e];
-    }
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const float2 m = __half22float2(ms[t]);  // (min, scale)
-      float x[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const uint32_t c = (is_k ? code[t] >> (4 * e) : w[e] >> (4 * t)) & 0xFu;
-        x[e] = __fadd_rn(__fmul_rn(static_cast<float>(c), m.y), m.x);
-      }
-      val[t] = pack16<VEC>(x);
+      for (int q = 0; q < 4; ++q) w[q] = __ldcg(src + q);
     }
   }
-  __half* dst = is_k ? a.k_out : a.v_out;
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    const int p = base + t;
-    if (p >= un.t0 && p < un.t1)
-      *reinterpret_cast<V*>(dst + static_cast<size_t>(un.row + p) * a.ld + head * D + e0) = val[t];
+    if (t < first || t >= last) continue;
+    uint4 lo, hi;
+    if (Q4) {
+      uint32_t ca[8], cb[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (is_k) {
+          ca[e] = (code[t].x >> (4 * e)) & 0xFu;
+          cb[e] = (code[t].y >> (4 * e)) & 0xFu;
+        } else {
+          const uint32_t wa = e & 3 ? (e & 3) == 1 ? w[e / 4].y : (e & 3) == 2 ? w[e / 4].z : w[e / 4].w : w[e / 4].x;
+          const uint4& v = w[2 + e / 4];
+          const uint32_t wb = e & 3 ? (e & 3) == 1 ? v.y : (e & 3) == 2 ? v.z : v.w : v.x;
+          ca[e] = (wa >> (4 * t)) & 0xFu;
+          cb[e] = (wb >> (4 * t)) & 0xFu;
+        }
+      }
+      const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&ms[t]));
+      lo = dequant_chunk(ca, m);
+      hi = dequant_chunk(cb, m);
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __half*>(is_k ? a.kv.k : a.kv.v) +
+                                                        (slot0 + t) * D + 16 * p);
+      lo = __ldcg(src);
+      hi = __ldcg(src + 1);
+    }
+    uint4* to = reinterpret_cast<uint4*>(dst + static_cast<size_t>(t) * a.ld);
+    to[0] = lo;
+    to[1] = hi;
   }
 }
+
+// Jobs of a block's K (and of its V): a warp's heads each.
+int kv_jobs_of(int kv_heads, int d) { return (kv_heads * (d / 16) + 31) / 32; }
 
 unsigned ctas(long long warps) { return static_cast<unsigned>((warps + kWarps - 1) / kWarps); }
 
@@ -352,8 +456,9 @@ unsigned ctas(long long warps) { return static_cast<unsigned>((warps + kWarps - 
 cudaError_t launch_paged_append(const PagedView& kv, const RaggedView& batch, const RopeView& rope, int heads, int d,
                                 int kv_bits, const __half* k, const __half* v, int ld, const __half* q, int ldq,
                                 __half* q_out, int ldqo, cudaStream_t s) {
-  AppendArgs a{kv, batch, rope, heads, k, v, ld, q, ldq, q_out, ldqo, 0, 0, runtime().err};
-  a.jobs = 2 * kv.kv_heads + (q != nullptr ? heads : 0);
+  AppendArgs a{kv, batch, rope, heads, k, v, ld, q, ldq, q_out, ldqo, kv_jobs_of(kv.kv_heads, d), 0, 0, runtime().err};
+  const int q_heads = 32 / (d / 16) * kQHeads;
+  a.jobs = 2 * a.kv_jobs + (q != nullptr ? (heads + q_heads - 1) / q_heads : 0);
   a.total = unit_count(batch) * a.jobs;
   const dim3 grid(ctas(a.total));
   if (kv_bits == 4)
@@ -365,8 +470,8 @@ cudaError_t launch_paged_append(const PagedView& kv, const RaggedView& batch, co
 
 cudaError_t launch_paged_read(const PagedView& kv, const RaggedView& batch, int d, int kv_bits, __half* k_out,
                               __half* v_out, int ld, cudaStream_t s) {
-  ReadArgs a{kv, batch, k_out, v_out, ld, 0, runtime().err};
-  a.total = unit_count(batch) * 2 * kv.kv_heads;
+  ReadArgs a{kv, batch, k_out, v_out, ld, kv_jobs_of(kv.kv_heads, d), 0, runtime().err};
+  a.total = unit_count(batch) * 2 * a.kv_jobs;
   const dim3 grid(ctas(a.total));
   if (kv_bits == 4)
     return d == 128 ? launch_pdl(paged_read_kernel<128, true>, grid, kWarps * 32, 0, s, a)
