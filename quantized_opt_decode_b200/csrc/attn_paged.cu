@@ -21,7 +21,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "paged.cuh"
 #include "warp_mma.cuh"
@@ -499,12 +498,13 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem<attn_paged_rows_kernel<D, Q4, NT>>(kMaxWarps * T::stages * T::bytes);
   if (e != cudaSuccess) return e;
   // Warps of a unit (its tiles go round them): what 16 warps an SM give it, but no more
-  // than it has tiles; two at least, so that a unit's fixed cost is shared.
+  // than it has tiles; four or, with very many units, two at the least, so that the fixed
+  // cost of a unit stays small (8064 units of 300 to 1040 keys: 205 us with two, 211 with four, 231
+  // with one).
   const long long units = static_cast<long long>(a.batch.b) * a.kv.kv_heads;
   const long long tiles = (a.batch.max_len + T::keys - 1) / T::keys;
   const long long ways = std::min(16ll * runtime().num_sms / units, tiles);
-  int warps = ways >= 8 ? 8 : ways >= 4 ? 4 : 2;
-  if (getenv("FQ_WARPS")) warps = atoi(getenv("FQ_WARPS"));
+  const int warps = ways >= 8 ? 8 : ways >= 4 || 2 * units < 64ll * runtime().num_sms ? 4 : 2;
   const int splits = static_cast<int>(std::max(1ll, std::min<long long>(kMaxCluster, ways / warps)));
   const int smem = warps * T::stages * T::bytes;
   cudaLaunchConfig_t cfg = {};

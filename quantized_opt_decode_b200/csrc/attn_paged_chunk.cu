@@ -96,25 +96,29 @@ struct Unit {
   int tiles;  // key tiles that some row of the unit sees
 };
 
-// The units of CTA (or cluster) `id` of `count`, in order: numbers id, id + count, ..,
-// 32 looked up at a time, one by each lane; those that hold no rows are passed over.
+// The units of CTA (or cluster) `id` of `count`, in order: one of each `count` unit
+// numbers, from the front and from the back by turns (long units tend to come first), 32 looked
+// up at a time, one by each lane; those that hold no rows are passed over.
 struct UnitWalk {
-  long long base, total, stride;
+  long long round, total;
+  int id, stride;
   uint32_t found;
   int i, head, row0, n, len, c0;
 
-  __device__ __forceinline__ void start(const ChunkArgs& a, int id, int count) {
+  __device__ __forceinline__ void start(const ChunkArgs& a, int id_, int count) {
     total = unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1) * a.kv.kv_heads;
+    id = id_;
     stride = count;
-    base = id;
+    round = 0;
     found = 0;
   }
   // Every lane of the warp calls this and gets the same unit; false: no more.
   __device__ __forceinline__ bool next(const ChunkArgs& a, Unit& out) {
     while (found == 0) {
-      if (base >= total) return false;
-      const long long w = base + stride * static_cast<int>(lane_id());
-      base += stride * 32;
+      if (round * stride >= total) return false;
+      const long long k = round + lane_id();
+      const long long w = k * stride + (k & 1 ? stride - 1 - id : id);
+      round += 32;
       found = __ballot_sync(0xffffffffu, w < total && look(a, static_cast<int>(w)));
     }
     const int from = __ffs(found) - 1;

@@ -23,11 +23,12 @@
 namespace flexq {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kUnitShift = 3;  // units of 8 tokens
 constexpr int kUnitExtra = 2;  // n tokens at any phase touch at most floor(n / 8) + 2 blocks
 
-constexpr int kQHeads = 4;       // heads of Q that a lane takes in turn
+constexpr int kQHeads = 4;  // heads of Q that a lane takes in turn
+constexpr int kQParts = 4;  // jobs that share a block's tokens of Q
 
 // Elements of a 16-byte chunk.
 __device__ __forceinline__ void unpack(const uint4& raw, float (&x)[8]) {
@@ -115,6 +116,16 @@ __device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+// x / 15 correctly rounded: the product with the rounded reciprocal is within an
+// ulp, its remainder is exact in one multiply-add, and one more with the reciprocal
+// rounds to the quotient (Markstein, 1990).  x: a difference of fp16 values, so
+// nothing underflows.
+__device__ __forceinline__ float fifteenth(float x) {
+  constexpr float y = 1.0f / 15.0f;
+  const float q = __fmul_rn(x, y);
+  return fmaf(fmaf(-15.0f, q, x), y, q);
+}
+
 struct Group {
   __half2 pair;  // (min, scale) as stored
   float mn, sc, inv;
@@ -122,7 +133,7 @@ struct Group {
 __device__ __forceinline__ Group group_of(uint32_t range) {
   const float lo = __fadd_rn(__half2float(__ushort_as_half(range & 0xffffu)), 0.0f);  // -0 -> +0
   const float hi = __fadd_rn(__half2float(__ushort_as_half((range >> 16) ^ 0x8000u)), 0.0f);
-  const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+  const __half s16 = __float2half_rn(fifteenth(__fsub_rn(hi, lo)));
   const __half m16 = __float2half_rn(lo);
   Group g;
   g.pair = __halves2half2(m16, s16);
@@ -132,12 +143,45 @@ __device__ __forceinline__ Group group_of(uint32_t range) {
   return g;
 }
 
-// Codes of a chunk.
-__device__ __forceinline__ void chunk_codes(const uint4& raw, const Group& g, uint32_t (&c)[8]) {
+// Codes of a chunk as the bits of 1.5 * 2^23 + code (0x4B400000 + code): adding that
+// number rounds to the nearest integer, half to even.  As in q64_code, the product with the
+// reciprocal stands in for the quotient wherever it is farther from a rounding boundary
+// than the two can differ (15 * 2^-20); within 2^-15 of one, which one chunk in some thousand
+// has, the chunk's quotients are computed.  x >= min, so codes are never negative;
+// a group whose scale was rounded down far (a subnormal one) needs the limit of 15.
+constexpr uint32_t kCodeBias = 0x4B400000u;
+__device__ __noinline__ void exact_codes(uint4 raw, float mn, float sc, uint32_t* c) {
   float x[8];
   unpack(raw, x);
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e)
+    c[e] = __float_as_uint(__fadd_rn(fminf(__fdiv_rn(__fsub_rn(x[e], mn), sc), 15.0f), 12582912.0f));
+}
+__device__ __forceinline__ void chunk_codes(const uint4& raw, const Group& g, uint32_t (&c)[8]) {
+  float x[8], far = 0.0f;
+  unpack(raw, x);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = g.sc != 0.0f ? q64_code(__fsub_rn(x[e], g.mn), g.sc, g.inv) : 0u;
+  for (int e = 0; e < 8; ++e) {
+    const float r = fminf(__fmul_rn(__fsub_rn(x[e], g.mn), g.inv), 15.0f);
+    const float k = __fadd_rn(r, 12582912.0f);
+    c[e] = __float_as_uint(k);
+    far = fmaxf(far, fabsf(__fsub_rn(r, __fsub_rn(k, 12582912.0f))));
+  }
+  if (far >= 0.5f - 0x1p-15f && g.sc != 0.0f) {
+    uint32_t exact[8];
+    exact_codes(raw, g.mn, g.sc, exact);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = exact[e];
+  }
+}
+
+// Eight such codes as a word, element e in nibble e: the biases add up to a constant.
+__device__ __forceinline__ uint32_t pack_codes(const uint32_t (&c)[8]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w += (c[e] << (4 * e));
+  constexpr uint32_t bias = kCodeBias * 0x11111111u;
+  return w - bias;
 }
 
 // The lane's two chunks quantized with their head's groups; every lane of the warp
@@ -163,10 +207,10 @@ __device__ __forceinline__ void quantize(const uint4& ra, const uint4& rb, const
       r0 = min2(r0, __shfl_xor_sync(0xffffffffu, r0, o));
       r1 = min2(r1, __shfl_xor_sync(0xffffffffu, r1, o));
     }
-    const Group ga = group_of(s.ea < 64 ? r0 : r1), gb = group_of(s.eb < 64 ? r0 : r1);
-    if (p < 2 && live) meta[p] = group_of(p == 0 ? r0 : r1).pair;
-    chunk_codes(ra, ga, ca);
-    chunk_codes(rb, gb, cb);
+    const Group g0 = group_of(r0), g1 = group_of(r1);
+    if (p < 2 && live) meta[p] = p == 0 ? g0.pair : g1.pair;
+    chunk_codes(ra, s.ea < 64 ? g0 : g1, ca);
+    chunk_codes(rb, s.eb < 64 ? g0 : g1, cb);
   }
 }
 
@@ -218,7 +262,7 @@ struct AppendArgs {
 enum Kind { kK, kV, kQ };
 
 template <int D, bool Q4>
-__global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 6) paged_append_kernel(const AppendArgs a) {
   constexpr int LH = D / 16;     // lanes of a head
   constexpr int HW = 32 / LH;    // heads of a warp at once
   constexpr int G = D / 64;
@@ -242,8 +286,9 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
   const Slot sl = slot_of(p, turn ? a.rope.rot_dim : 0, inter);
 
   if (kind == kQ) {
-    const int h0 = job * HW * kQHeads + lane / LH;
-    for (int t = un.t0; t < un.t1; ++t) {
+    const int h0 = job / kQParts * HW * kQHeads + lane / LH;
+    const int first = (un.t0 & ~7) + job % kQParts * (8 / kQParts);
+    for (int t = max(un.t0, first); t < min(un.t1, first + 8 / kQParts); ++t) {
       const size_t row = static_cast<size_t>(un.row + t);
       uint4 ra[kQHeads], rb[kQHeads];
 #pragma unroll
@@ -280,26 +325,20 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
   if (page < 0) return;
   const size_t slot0 = pool_slot(a.kv, page, live ? head : 0, base);
   const __half* src = (kind == kK ? a.k : a.v) + (live ? head : 0) * D;
-  // V's words of 16 dimensions: kept where the new tokens cover the block only in part
+  // V's words of 16 dimensions; where the new tokens cover the block only in part, the
+  // others' codes are merged in at the end (loaded here, so that the rows' loads overlap)
   uint32_t w[16];
+  uint4 old[4];
   uint4* words = reinterpret_cast<uint4*>(static_cast<uint32_t*>(a.kv.v) + (slot0 >> 3) * D + 16 * p);
-  if (Q4 && kind == kV) {
+  const bool merge = Q4 && kind == kV && un.t1 - un.t0 < 8;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = 0u;
-    if (un.t1 - un.t0 < 8) {
-      uint32_t kept = 0xffffffffu;
-      kept &= ~(((1ull << (4 * (un.t1 - un.t0))) - 1) << (4 * (un.t0 - base)));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 old = words[q];
-        w[4 * q] = old.x & kept;
-        w[4 * q + 1] = old.y & kept;
-        w[4 * q + 2] = old.z & kept;
-        w[4 * q + 3] = old.w & kept;
-      }
-    }
+  for (int q = 0; q < 4; ++q) {
+    old[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (merge) old[q] = words[q];
   }
-  constexpr int B = 2;  // tokens in flight
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = 0u;
+  constexpr int B = Q4 ? 1 : 2;  // tokens in flight (4-bit: more warps instead, by the registers)
   for (int t = un.t0; t < un.t1; t += B) {
     uint4 ra[B], rb[B];
 #pragma unroll
@@ -334,22 +373,25 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
       if (kind == kK) {
         if (live) {
           uint8_t* dst = static_cast<uint8_t*>(a.kv.k) + slot * (D / 2);
-          *reinterpret_cast<uint32_t*>(dst + sl.ea / 2) = pack_canonical(ca);
-          *reinterpret_cast<uint32_t*>(dst + sl.eb / 2) = pack_canonical(cb);
+          *reinterpret_cast<uint32_t*>(dst + sl.ea / 2) = pack_codes(ca);
+          *reinterpret_cast<uint32_t*>(dst + sl.eb / 2) = pack_codes(cb);
         }
       } else {
         const int sh = 4 * (t + i - base);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          w[e] |= ca[e] << sh;
-          w[8 + e] |= cb[e] << sh;
+          w[e] += (ca[e] - kCodeBias) << sh;
+          w[8 + e] += (cb[e] - kCodeBias) << sh;
         }
       }
     }
   }
   if (Q4 && kind == kV && live) {
+    const uint32_t kept = ~static_cast<uint32_t>(((1ull << (4 * (un.t1 - un.t0))) - 1) << (4 * (un.t0 - base)));
 #pragma unroll
-    for (int q = 0; q < 4; ++q) words[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    for (int q = 0; q < 4; ++q)
+      words[q] = make_uint4(w[4 * q] | (old[q].x & kept), w[4 * q + 1] | (old[q].y & kept),
+                            w[4 * q + 2] | (old[q].z & kept), w[4 * q + 3] | (old[q].w & kept));
   }
 }
 
@@ -458,7 +500,7 @@ cudaError_t launch_paged_append(const PagedView& kv, const RaggedView& batch, co
                                 __half* q_out, int ldqo, cudaStream_t s) {
   AppendArgs a{kv, batch, rope, heads, k, v, ld, q, ldq, q_out, ldqo, kv_jobs_of(kv.kv_heads, d), 0, 0, runtime().err};
   const int q_heads = 32 / (d / 16) * kQHeads;
-  a.jobs = 2 * a.kv_jobs + (q != nullptr ? (heads + q_heads - 1) / q_heads : 0);
+  a.jobs = 2 * a.kv_jobs + (q != nullptr ? (heads + q_heads - 1) / q_heads * kQParts : 0);
   a.total = unit_count(batch) * a.jobs;
   const dim3 grid(ctas(a.total));
   if (kv_bits == 4)
