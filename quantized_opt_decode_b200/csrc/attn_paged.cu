@@ -248,8 +248,8 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
           const int x = 2 * km + h, y = x + 4 * (r & 1);  // y: token in its block
           const uint8_t* kb = st + (r >> 1) * 8 * T::row;
           const uint32_t ms = lds32(st + 2 * T::side + ((r >> 1) * 8 + y) * (D / 64) * 4 + (D == 128 ? (j >> 1) * 4 : 0));
-          mn[h] = __low2half2(as_half2(ms));
-          sc[h] = __high2half2(as_half2(ms));
+          mn[h] = dup_half(ms, 0);
+          sc[h] = dup_half(ms, 1);
           if (D == 128) {
             cw[h] = lds128(kb + ((y * 4 + j) ^ ((r & 1) * 4)) * 16);
           } else {

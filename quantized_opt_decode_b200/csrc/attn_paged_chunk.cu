@@ -267,16 +267,6 @@ __device__ __forceinline__ uint4 ldg128(const void* p) { return __ldcg(reinterpr
 __device__ __forceinline__ uint32_t ldg32(const void* p) { return __ldcg(reinterpret_cast<const unsigned int*>(p)); }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
-// mbar_wait without the call: roles that differ in registers cannot share a function.
-__device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity, uint64_t limit_ns) {
-  if (mbar_test(b, parity)) return true;
-  if (limit_ns < 1000) return false;  // (a test's limit: the first probe decides)
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(b, parity))
-    if (globaltimer_ns() - t0 > limit_ns) return false;
-  return true;
-}
-
 // Byte offset of 16-byte chunk c (0..7) of a row of a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t sw128(int row, int c) {
   return static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
@@ -341,7 +331,7 @@ struct Loader<D, true> {
     for (int q = 0; q < NQ; ++q) {
       const int y = sub / units, u = sub % units;
       const int row = block(q) * 8 + (y < 4 ? 2 * y : 2 * y - 7);
-      const __half2 mn = __low2half2(as_half2(km[q])), sc = __high2half2(as_half2(km[q]));
+      const __half2 mn = dup_half(km[q], 0), sc = dup_half(km[q], 1);
       // words in pairwise swapped order for half the units: eight lanes then hit
       // eight bank groups
       const bool swap = D == 128 && (u & 2);

@@ -5,10 +5,10 @@
 // The weight is read once (n k / 2 bytes of codes and n k / 16 of pairs) and that
 // is the bound; the rows of X are the B operand of mma.sync (8 columns an
 // instruction, one or two of them), so the arithmetic does not grow with m.  A CTA
-// owns one 128-feature tile of the weight, whose k-blocks are contiguous: a ninth warp
-// streams them through a ring, one bulk copy a stage of four blocks, with X's columns of
-// the stage beside them (16-byte copies that arrive on the same barrier); eight warps
-// take 32 features of every other block each and dequantize their rows' words into A
+// owns one 128-feature tile of the weight, whose k-blocks are contiguous: one warp
+// streams them through a ring, one bulk copy a stage, with X's columns of
+// the stage beside them (16-byte copies that arrive on the same barrier); each of the other warps
+// takes 32 features and two blocks of a stage and dequantizes its rows' words into A
 // fragments.  Where there are fewer tiles than SMs the K axis is shared out over a
 // cluster, whose sums are joined over distributed shared memory in a fixed order.
 //
@@ -24,13 +24,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8;  // 32 features each, of the even or the odd k-blocks
-constexpr int kHalves = 2;
-constexpr int kMT = 2;  // 16-feature tiles of a warp
-constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kBlocks = 4;  // k-blocks of a stage
-constexpr int kWBytes = kBlocks * kTileBytes;
-constexpr int kXRow = kBlocks * 128 + 16;  // a row of X in a stage; the pad keeps fragment reads free of bank conflicts
+constexpr int kMT = 2;     // 16-feature tiles of a warp: four warps side by side cover a block
+constexpr int kParts = 2;  // fours of warps, which take a stage's k-blocks by turns
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
@@ -53,19 +48,26 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Stages of the ring: two or three CTAs' worth of 18 KB weight copies in flight on an SM.
+// NT column tiles of 8 rows of X.  (Sixteen warps where one or two CTAs have an SM to
+// themselves measured 35.3 against 36.0 us at 5 rows, 28672 x 7168: not kept.)
 template <int NT>
-struct Ring {
+struct Shape {
+  static constexpr int warps = 4 * kParts, threads = (warps + 1) * 32;
+  static constexpr int blocks = 2 * kParts;  // k-blocks of a stage
+  static constexpr int w_bytes = blocks * kTileBytes;
+  static constexpr int x_row = blocks * 128 + 16;  // (the pad keeps fragment reads free of bank conflicts)
   static constexpr int stages = NT == 1 ? 3 : 2;
-  static constexpr int stage_bytes = kWBytes + 8 * NT * kXRow;
+  static constexpr int stage_bytes = w_bytes + 8 * NT * x_row;
   static constexpr int smem = stages * stage_bytes;
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) {
+__global__ void __launch_bounds__(Shape<NT>::threads, 3) gemv_q4_kernel(const GemvArgs a) {
+  using Sh = Shape<NT>;
   constexpr int LD = kTileRows + 4;  // floats of a row of sums
-  constexpr int kStages = Ring<NT>::stages, kStageBytes = Ring<NT>::stage_bytes;
-  static_assert(kHalves * 8 * NT * LD * 4 <= Ring<NT>::smem, "the sums lie over the ring");
+  constexpr int kWarps = Sh::warps, kThreads = Sh::threads, kBlocks = Sh::blocks, kStages = Sh::stages;
+  constexpr int kStageBytes = Sh::stage_bytes;
+  static_assert(kParts * 8 * NT * LD * 4 <= Sh::smem, "the sums lie over the ring");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int s_fail;
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
   const int steps = (kb1 - kb0 + kBlocks - 1) / kBlocks;
   const int r = lane >> 2, j = lane & 3;
   auto wait = [&](uint64_t* b, uint32_t parity, uint32_t code) {
-    if (mbar_wait(b, parity, a.limit_ns)) return true;
+    if (wait_phase(b, parity, a.limit_ns)) return true;
     set_error(a.err, code);
     atomicExch(&s_fail, 1);
     return false;
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-  const int feat = (warp & 3) * 32, half = warp >> 2;
+  const int feat = (warp & 3) * 32, part = warp >> 2;
 
   if (warp == kWarps) {
     const uint8_t* src = a.w + (static_cast<size_t>(tile) * kbs + kb0) * kTileBytes;
@@ -115,41 +117,40 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
       const int nb = min(kBlocks, kb1 - kb0 - s * kBlocks);
       if (lane == 0) {
         mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(nb) * kTileBytes);
-        bulk_load(st, src + static_cast<size_t>(s) * kWBytes, static_cast<uint32_t>(nb) * kTileBytes, &full[slot], policy);
+        bulk_load(st, src + static_cast<size_t>(s) * Sh::w_bytes, static_cast<uint32_t>(nb) * kTileBytes, &full[slot], policy);
       }
-      if (lane < nb * 8) {
-        const __half* xs = a.x + (kb0 + s * kBlocks) * 64 + lane * 8;
-        const uint32_t to = smem_u32(st + kWBytes + lane * 16);
+      for (int u = lane; u < nb * 8; u += 32) {
+        const __half* xs = a.x + (kb0 + s * kBlocks) * 64 + u * 8;
+        const uint32_t to = smem_u32(st + Sh::w_bytes + u * 16);
 #pragma unroll
         for (int i = 0; i < 8 * NT; ++i)
-          if (i < a.m) cp_async16(to + i * kXRow, xs + static_cast<size_t>(i) * a.ldx, true);
+          if (i < a.m) cp_async16(to + i * Sh::x_row, xs + static_cast<size_t>(i) * a.ldx, true);
       }
       cp_async_arrive(&full[slot]);
     }
     // no copy is in flight when the CTA lets go of its shared memory
     for (int d = max(0, s - kStages); d < s; ++d)
-      if (!mbar_wait(&full[d % kStages], (d / kStages) & 1, kDrainNs)) set_error(a.err, DEV_TIMEOUT_PRODUCER);
+      if (!wait_phase(&full[d % kStages], (d / kStages) & 1, kDrainNs)) set_error(a.err, DEV_TIMEOUT_PRODUCER);
   } else {
     // lane (r, j): features feat + r, + 8, + 16, + 24, columns 16 j .. 16 j + 15 of a k-block,
     // rows r (and r + 8) of X; what stands in rows past m are columns of the product that
     // nobody reads
-    const uint8_t* codes = smem + (feat + r) * 32 + j * 8 + half * kTileBytes;
-    const uint8_t* pairs = smem + kTileCodeBytes + (feat + r) * 4 + half * kTileBytes;
-    const uint8_t* xcols = smem + kWBytes + r * kXRow + j * 32 + half * 128;
+    const uint8_t* codes = smem + (feat + r) * 32 + j * 8 + part * kTileBytes;
+    const uint8_t* pairs = smem + kTileCodeBytes + (feat + r) * 4 + part * kTileBytes;
+    const uint8_t* xcols = smem + Sh::w_bytes + r * Sh::x_row + j * 32 + part * 128;
     auto block = [&](int slot, int b) {
       const int at = slot * kStageBytes + b * kTileBytes, xat = slot * kStageBytes + b * 128;
       uint4 x[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] = lds128(xcols + xat + nt * 8 * kXRow);
-        x[nt][1] = lds128(xcols + xat + nt * 8 * kXRow + 16);
+        x[nt][0] = lds128(xcols + xat + nt * 8 * Sh::x_row);
+        x[nt][1] = lds128(xcols + xat + nt * 8 * Sh::x_row + 16);
       }
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
         const uint2 c0 = lds64(codes + at + mt * 512), c1 = lds64(codes + at + mt * 512 + 256);
         const uint32_t p0 = lds32(pairs + at + mt * 64), p1 = lds32(pairs + at + mt * 64 + 32);
-        const __half2 h0 = *reinterpret_cast<const __half2*>(&p0), h1 = *reinterpret_cast<const __half2*>(&p1);
-        const __half2 m0 = __low2half2(h0), s0 = __high2half2(h0), m1 = __low2half2(h1), s1 = __high2half2(h1);
+        const __half2 m0 = dup_half(p0, 0), s0 = dup_half(p0, 1), m1 = dup_half(p1, 0), s1 = dup_half(p1, 1);
 #pragma unroll
         for (int wd = 0; wd < 2; ++wd) {
           uint32_t lo[4], hi[4];
@@ -168,10 +169,10 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
     for (int s = 0; s < steps; ++s) {
       ok = __all_sync(0xffffffffu, wait(&full[slot], parity, DEV_TIMEOUT_CONSUMER));
       if (!ok) break;
-      const int nb = kb1 - kb0 - s * kBlocks - half;  // blocks from the warp's first of the stage on
-      if (nb > kHalves) {
+      const int nb = kb1 - kb0 - s * kBlocks - part;  // blocks from the warp's first of the stage on
+      if (nb > kParts) {
         block(slot, 0);
-        block(slot, kHalves);
+        block(slot, kParts);
       } else if (nb > 0) {
         block(slot, 0);
       }
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
   __syncthreads();
   pdl_trigger();
 
-  // the tile's sums [half][rows of X][128 features] over the ring
+  // the tile's sums [part][rows of X][128 features] over the ring
   float* sums = reinterpret_cast<float*>(smem);
   if (warp < kWarps) {
 #pragma unroll
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          sums[(half * 8 * NT + nt * 8 + 2 * j + (e & 1)) * LD + feat + mt * 16 + (e >> 1) * 8 + r] = acc[mt][nt][e];
+          sums[(part * 8 * NT + nt * 8 + 2 * j + (e & 1)) * LD + feat + mt * 16 + (e >> 1) * 8 + r] = acc[mt][nt][e];
   }
   bool fine = true;
   if (splits == 1) {
@@ -212,16 +213,19 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
     if (col >= a.n) continue;
     float v = 0.f;
     if (splits == 1) {
-      v = sums[row * LD + f] + sums[(8 * NT + row) * LD + f];
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) v += sums[(q * 8 * NT + row) * LD + f];
     } else {
-      float part[kMaxCluster];
+      float sum[kMaxCluster];
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
-        const float* s0 = cluster.map_shared_rank(sums, c < splits ? c : 0) + row * LD + f;
-        part[c] = c < splits ? s0[0] + s0[8 * NT * LD] : 0.f;
+        const float* from = cluster.map_shared_rank(sums, c < splits ? c : 0) + row * LD + f;
+        sum[c] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) sum[c] += c < splits ? from[q * 8 * NT * LD] : 0.f;
       }
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) v += part[c];
+      for (int c = 0; c < kMaxCluster; ++c) v += sum[c];
     }
     if (a.epi & EPI_BIAS) v += __half2float(a.bias[col]);
     if (a.epi & EPI_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
@@ -239,16 +243,17 @@ __global__ void __launch_bounds__(kThreads, 3) gemv_q4_kernel(const GemvArgs a) 
 
 template <int NT>
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t s) {
-  cudaError_t e = allow_smem<gemv_q4_kernel<NT>>(Ring<NT>::smem);
+  using Sh = Shape<NT>;
+  cudaError_t e = allow_smem<gemv_q4_kernel<NT>>(Sh::smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.n + kTileRows - 1) / kTileRows, kbs = a.k / 64;
-  // the K axis over a cluster while SMs would have nothing to do and each CTA keeps a stage's half
+  // the K axis over a cluster while SMs would have nothing to do and each CTA keeps two blocks
   int splits = 1;
-  while (splits < kMaxCluster && tiles * splits < runtime().num_sms && kbs >= 2 * splits * (kBlocks / 2)) splits *= 2;
+  while (splits < kMaxCluster && tiles * splits < runtime().num_sms && kbs >= 4 * splits) splits *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * splits);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Ring<NT>::smem;
+  cfg.blockDim = dim3(Sh::threads);
+  cfg.dynamicSmemBytes = Sh::smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -65,6 +65,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// The low (0) or high (1) half of a pair, twice.
+__device__ __forceinline__ __half2 dup_half(uint32_t x, int which) {
+  const uint32_t y = __byte_perm(x, x, which ? 0x3232 : 0x1010);
+  return *reinterpret_cast<const __half2*>(&y);
+}
+
 // The eight codes of a word as four fp16 pairs (code i, code i + 4), i = 0..3,
 // dequantized: code * scale + min rounded once to fp16 (the codec rounds the
 // product, exact in fp32, plus min to fp32 and then to fp16: the same value
@@ -97,6 +103,17 @@ __device__ __forceinline__ void dequant_word(uint32_t w, __half2 s0, __half2 m0,
 // One scale and min for the whole word.
 __device__ __forceinline__ void dequant_word(uint32_t w, __half2 s, __half2 m, uint32_t (&out)[4]) {
   dequant_word(w, s, m, s, m, s, m, s, m, out);
+}
+
+// mbar_wait without a call: registers stay where they are, and roles that
+// differ in their register counts can share it.
+__device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_test(b, parity)) return true;
+  if (limit_ns < 1000) return false;  // (a test's limit: the first probe decides)
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(b, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
 }
 
 // Opts a kernel in to `bytes` of dynamic shared memory, once per device
