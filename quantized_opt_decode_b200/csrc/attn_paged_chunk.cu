@@ -455,7 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   UnitWalk walk;
   Unit un;
   walk.start(a, blockIdx.x / splits, gridDim.x / splits);
-  if (!walk.next(a, un)) return;  // (every warp of the cluster alike)
+  const bool any = walk.next(a, un);
+  if (blockIdx.x == 0 && warp == kMmaWarp + 1) check_spans(a.batch, a.err);
+  if (!any) return;  // (every warp of the cluster alike)
 
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);

@@ -29,6 +29,12 @@ __device__ __forceinline__ Span ragged_span(const RaggedView& r, int i, uint32_t
   return s;
 }
 
+// Looks at every sequence, by one warp: a start table that decreases gives some of them no unit,
+// and they are to be reported all the same.
+__device__ __forceinline__ void check_spans(const RaggedView& r, uint32_t* err) {
+  for (int i = static_cast<int>(lane_id()); i < r.b; i += 32) ragged_span(r, i, err);
+}
+
 __device__ __forceinline__ long long unit_base(const RaggedView& r, int i, int scale, int shift, int extra) {
   return unit_base_at(r.row_start[i], i, scale, shift, extra);
 }

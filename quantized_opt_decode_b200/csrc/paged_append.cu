@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kWarps * 32, 6) paged_append_kernel(const Appe
   constexpr int G = D / 64;
   pdl_wait();
   const long long widx = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (widx == 0 && a.batch.max_new > 1) check_spans(a.batch, a.err);
   if (widx >= a.total) return;
   const int lane = static_cast<int>(lane_id());
   Unit un;
@@ -420,6 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_read_kernel(const ReadArgs 
   constexpr int LH = D / 16, HW = 32 / LH, G = D / 64;
   pdl_wait();
   const long long widx = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (widx == 0 && a.batch.max_new > 1) check_spans(a.batch, a.err);
   if (widx >= a.total) return;
   const int lane = static_cast<int>(lane_id());
   const int jobs = 2 * a.kv_jobs;

@@ -188,6 +188,28 @@ def test_attention_against_64_bits(bits, heads, kv_heads, d, page, new, past):
     check_attention(pg, q, to_host(out))
 
 
+SHARED = [
+    # long histories of few units, which are shared out over a cluster; groups of more than 16
+    # heads; both row tiles and one, of a unit; sequences on either side of the few-row limit
+    (4, 24, 1, 128, 16, (1,), (3000,)),
+    (16, 32, 1, 64, 32, (3, 1), (5000, 70)),
+    (4, 2, 2, 64, 256, (40,), (9000,)),
+    (4, 2, 2, 128, 64, (9, 8, 1), (4100, 2000, 7000)),
+    (16, 4, 2, 128, 128, (300,), (2500,)),
+    (16, 2, 2, 128, 16, (130, 1), (3000, 6000)),
+    (4, 20, 1, 64, 8, (1, 2, 0, 13), (129, 640, 50, 0)),
+    (4, 14, 2, 128, 32, (2, 3, 1), (500, 31, 64)),
+    (4, 12, 1, 128, 16, (1, 1), (15000, 10)),
+    (4, 71, 1, 64, 64, (1, 30), (700, 3)),
+    (16, 17, 1, 128, 8, (1, 1), (64, 63)),
+]
+
+
+@pytest.mark.parametrize("bits,heads,kv_heads,d,page,new,past", SHARED)
+def test_attention_of_shared_out_histories_and_wide_groups(bits, heads, kv_heads, d, page, new, past):
+    test_attention_against_64_bits(bits, heads, kv_heads, d, page, new, past)
+
+
 @pytest.mark.parametrize("bits", [4, 16])
 @pytest.mark.parametrize("scale", [0.0, 1e-4, 12.0])
 @pytest.mark.parametrize("new,past", [((1, 1), (300, 17)), ((70, 3), (90, 5))])

@@ -36,7 +36,7 @@ COMMON = [(dict(kv_heads=3), "kv_heads"), (dict(kv_heads=0), "kv_heads"), (dict(
           (dict(v_meta=A + 4), "k_meta"), (dict(b=-1), "b and rows"), (dict(rows=-1), "b and rows"),
           (dict(b=70000), "65535"), (dict(table=None), "table"), (dict(row_start=None), "row_start"),
           (dict(kv_len=A + 2), "kv_len"), (dict(max_new=0), "max_new"), (dict(max_len=0), "max_len"),
-          (dict(max_len=65), "exceeds a table row"), (dict(table_ld=0), "exceeds a table row"), (dict(heads=3), "heads")]
+          (dict(rows=1 << 24, h=8192, heads=128), "rows * heads"), (dict(max_len=65), "exceeds a table row"), (dict(table_ld=0), "exceeds a table row"), (dict(heads=3), "heads")]
 
 
 @pytest.mark.parametrize("over,word", COMMON)
