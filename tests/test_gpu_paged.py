@@ -200,7 +200,7 @@ SHARED = [
     (4, 20, 1, 64, 8, (1, 2, 0, 13), (129, 640, 50, 0)),
     (4, 14, 2, 128, 32, (2, 3, 1), (500, 31, 64)),
     (4, 12, 1, 128, 16, (1, 1), (15000, 10)),
-    (4, 71, 1, 64, 64, (1, 30), (700, 3)),
+    (4, 70, 1, 64, 64, (1, 30), (700, 3)),
     (16, 17, 1, 128, 8, (1, 1), (64, 63)),
 ]
 
