@@ -48,13 +48,21 @@ __device__ __forceinline__ uint4 pack16(const float (&x)[8]) {
   return raw;
 }
 
-// The two chunks of lane p of a head: dimensions ea .. ea + 7 and eb .. eb + 7.
+// The two chunks of lane p of a head: dimensions ea .. ea + 7 and eb .. eb + 7.  Without
+// rotation they lie half a head apart, so that eight lanes' chunks are 128 bytes in a row.
 struct Slot {
   int ea, eb;
   bool turned;
 };
+template <int D>
 __device__ __forceinline__ Slot slot_of(int p, int rot, bool interleaved) {
   Slot s;
+  if (rot == 0) {
+    s.turned = false;
+    s.ea = 8 * p;
+    s.eb = D / 2 + 8 * p;
+    return s;
+  }
   s.turned = p < rot / 16;
   s.ea = s.turned && !interleaved ? 8 * p : 16 * p;
   s.eb = s.turned && !interleaved ? rot / 2 + 8 * p : 16 * p + 8;
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, 6) paged_append_kernel(const Appe
     if (lane == 0) set_error(a.err, DEV_BAD_ARGUMENT);
     return;
   }
-  const Slot sl = slot_of(p, turn ? a.rope.rot_dim : 0, inter);
+  const Slot sl = slot_of<D>(p, turn ? a.rope.rot_dim : 0, inter);
 
   if (kind == kQ) {
     const int h0 = job / kQParts * HW * kQHeads + lane / LH;
@@ -330,12 +338,13 @@ __global__ void __launch_bounds__(kWarps * 32, 6) paged_append_kernel(const Appe
   // others' codes are merged in at the end (loaded here, so that the rows' loads overlap)
   uint32_t w[16];
   uint4 old[4];
-  uint4* words = reinterpret_cast<uint4*>(static_cast<uint32_t*>(a.kv.v) + (slot0 >> 3) * D + 16 * p);
+  uint32_t* block = static_cast<uint32_t*>(a.kv.v) + (slot0 >> 3) * D;
+  auto word4 = [&](int q) { return reinterpret_cast<uint4*>(block + (q < 2 ? sl.ea + 4 * q : sl.eb + 4 * (q - 2))); };
   const bool merge = Q4 && kind == kV && un.t1 - un.t0 < 8;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     old[q] = make_uint4(0u, 0u, 0u, 0u);
-    if (merge) old[q] = words[q];
+    if (merge) old[q] = *word4(q);
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) w[e] = 0u;
@@ -391,8 +400,8 @@ __global__ void __launch_bounds__(kWarps * 32, 6) paged_append_kernel(const Appe
     const uint32_t kept = ~static_cast<uint32_t>(((1ull << (4 * (un.t1 - un.t0))) - 1) << (4 * (un.t0 - base)));
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      words[q] = make_uint4(w[4 * q] | (old[q].x & kept), w[4 * q + 1] | (old[q].y & kept),
-                            w[4 * q + 2] | (old[q].z & kept), w[4 * q + 3] | (old[q].w & kept));
+      *word4(q) = make_uint4(w[4 * q] | (old[q].x & kept), w[4 * q + 1] | (old[q].y & kept),
+                             w[4 * q + 2] | (old[q].z & kept), w[4 * q + 3] | (old[q].w & kept));
   }
 }
 
@@ -436,24 +445,36 @@ __global__ void __launch_bounds__(kWarps * 32) paged_read_kernel(const ReadArgs 
   if (page < 0 || head >= a.kv.kv_heads) return;
   const size_t slot0 = pool_slot(a.kv, page, head, base);
   const int first = un.t0 - base, last = un.t1 - base;
-  __half* dst = (is_k ? a.k_out : a.v_out) + static_cast<long long>(un.row + base) * a.ld + head * D + 16 * p;
+  // the lane's two chunks lie half a head apart: eight lanes store 128 bytes in a row, and with
+  // d = 128 the second chunk is in the second group
+  __half* dst = (is_k ? a.k_out : a.v_out) + static_cast<long long>(un.row + base) * a.ld + head * D + 8 * p;
   uint4 w[4];     // V: the block's words of 16 dimensions
   uint2 code[8];  // K: 16 codes of each token
-  uint32_t ms[8];
+  uint2 ms[8];    // (min, scale) of the two chunks
   if (Q4) {
-    const char* meta = static_cast<const char*>(is_k ? a.kv.k_meta : a.kv.v_meta) + (slot0 * G + p / 4) * 4;
+    const char* meta = static_cast<const char*>(is_k ? a.kv.k_meta : a.kv.v_meta) + slot0 * G * 4;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
-      if (t >= first && t < last) ms[t] = __ldcg(reinterpret_cast<const unsigned int*>(meta + t * G * 4));
+      if (t >= first && t < last) {
+        if (G == 2) {
+          ms[t] = __ldcg(reinterpret_cast<const uint2*>(meta + t * 8));
+        } else {
+          ms[t].x = __ldcg(reinterpret_cast<const unsigned int*>(meta + t * 4));
+          ms[t].y = ms[t].x;
+        }
+      }
     if (is_k) {
-      const char* src = static_cast<const char*>(a.kv.k) + slot0 * (D / 2) + 8 * p;
+      const char* src = static_cast<const char*>(a.kv.k) + slot0 * (D / 2) + 4 * p;
 #pragma unroll
       for (int t = 0; t < 8; ++t)
-        if (t >= first && t < last) code[t] = __ldcg(reinterpret_cast<const uint2*>(src + t * (D / 2)));
+        if (t >= first && t < last) {
+          code[t].x = __ldcg(reinterpret_cast<const unsigned int*>(src + t * (D / 2)));
+          code[t].y = __ldcg(reinterpret_cast<const unsigned int*>(src + t * (D / 2) + D / 4));
+        }
     } else {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(a.kv.v) + (slot0 >> 3) * D + 16 * p);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(a.kv.v) + (slot0 >> 3) * D + 8 * p);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = __ldcg(src + q);
+      for (int q = 0; q < 4; ++q) w[q] = __ldcg(src + (q < 2 ? q : D / 8 + q - 2));
     }
   }
 #pragma unroll
@@ -475,18 +496,17 @@ __global__ void __launch_bounds__(kWarps * 32) paged_read_kernel(const ReadArgs 
           cb[e] = (wb >> (4 * t)) & 0xFu;
         }
       }
-      const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&ms[t]));
-      lo = dequant_chunk(ca, m);
-      hi = dequant_chunk(cb, m);
+      lo = dequant_chunk(ca, __half22float2(*reinterpret_cast<const __half2*>(&ms[t].x)));
+      hi = dequant_chunk(cb, __half22float2(*reinterpret_cast<const __half2*>(&ms[t].y)));
     } else {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __half*>(is_k ? a.kv.k : a.kv.v) +
-                                                        (slot0 + t) * D + 16 * p);
+                                                        (slot0 + t) * D + 8 * p);
       lo = __ldcg(src);
-      hi = __ldcg(src + 1);
+      hi = __ldcg(src + D / 16);
     }
     uint4* to = reinterpret_cast<uint4*>(dst + static_cast<size_t>(t) * a.ld);
     to[0] = lo;
-    to[1] = hi;
+    to[D / 16] = hi;
   }
 }
 
