@@ -17,6 +17,14 @@
 // where one unit's history is shared out, take tiles in turn.  Their (maximum, sum,
 // output) are joined in a fixed order: in shared memory, then over the cluster's
 // distributed shared memory, so the call needs no workspace.
+//
+// Measured (B200): 144 sequences of 300 to 1040 keys, 56 heads, d = 128, 4 bit: 201 to 214 us from box to
+// box for 788 MB, 0.57 to 0.60 of the copy rate; five of 18900 to 32700 keys, 8 key/value heads: 58 us for
+// 149 MB (the clusters are alike, the histories are not: the longest is 1.3 times the mean); one fp16
+// sequence of 902 keys, 32 heads, d = 64: 5.8 us, the launch.  The 4-bit form is bound by the half-precision
+// pipe that the dequantizer's eight multiply-adds and the mma.sync of a word share: 23 cycles a
+// word and scheduler alone in a loop, 750 cycles a tile of the 1150 that it takes.  Three quarters of
+// the registers (18 warps an SM) gained nothing (214 us), nor did two stages instead of three.
 #include <cooperative_groups.h>
 #include <math.h>
 

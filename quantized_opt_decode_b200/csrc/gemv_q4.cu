@@ -12,9 +12,15 @@
 // fragments.  Where there are fewer tiles than SMs the K axis is shared out over a
 // cluster, whose sums are joined over distributed shared memory in a fixed order.
 //
-// With one warp a K slice and 32 features, each with its own ring of 16-byte copies, the
-// same sums took 41 us (5 rows, 28672 x 7168) and 50 us (16 rows, 50272 x 4096): 600
-// instructions a warp for 2304 bytes, more than half of them addresses and copies of X.
+// Measured (B200): 5 rows, 28672 x 7168: 37 us for 116 MB, 0.47 of the copy rate; 16 rows, 50272 x 4096:
+// 41 us for 119 MB; one row, 2048 x 2048: 5.0 us, the launch.  Bound by the half-precision pipe that the
+// dequantizer's multiply-adds and mma.sync share (190 of the 290 cycles that four warps take
+// for a k-block), and by 224 tiles on 148 SMs: two on some, one on others; sharing K out more finely cost
+// more than it evened out (38 us with two parts, 51 with eight).  Tried: a warp a K slice with its own ring of
+// 16-byte copies (41 and 50 us: 600 instructions for 2304 bytes, half of them addresses and copies
+// of X); X through the L1 cache (36 and 47 us); the dequantized rows in tensor memory and the products on
+// tcgen05 (42 and 38 us, 6.3 instead of 5.0 us for the small one: the hand-offs between the
+// warps cost what the products had).
 #include <cooperative_groups.h>
 
 #include "warp_mma.cuh"

@@ -12,7 +12,12 @@
 // spread over the 8 (d = 128) or 4 lanes of the head: its minimum and maximum are one
 // shuffle ladder a group on the pair (min x, -max x) in two fp16 halves.
 //
-// Memory bounds both kernels: rows in, codes and pairs out, and for Q rows in and out.
+// Memory is the floor of both kernels: rows in, codes and pairs out, and for Q rows in and
+// out.  Measured (B200): 8345 rows of 8 key/value and 32 query heads, d = 128, rotated, to 4 bit:
+// 46 us for 175 MB (the quantizer's 28 instructions an element of K and V take half the issue
+// slots; prefetched rows, or more or fewer warps an SM, changed nothing); 2055 rows to fp16, d = 64: 12.5 us for
+// 51 MB; reading 19085 tokens of 32 heads back: 73 us for 401 MB, 0.84 of the copy rate (82 us with a
+// lane's two chunks side by side, which its stores then half fill).
 //
 // The codes are exactly those of flexq_quantize on the (rotated) fp16 rows:
 // rotation multiplies and adds in fp32 without contraction and rounds once to
