@@ -422,13 +422,18 @@ struct ReadArgs {
 
 // Eight codes of a word (element e in nibble e) as the codec's fp16 values: the
 // product with the scale is exact in fp32, so one multiply-add rounds as the codec's two
-// operations do.  (c | 0x4B000000) is the fp32 value 2^23 + c.
+// operations do.  c[e]: 0x4B000000 + code, the fp32 value 2^23 + code.
 __device__ __forceinline__ uint4 dequant_chunk(const uint32_t (&c)[8], float2 ms) {
   float x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = fmaf(__uint_as_float(c[e] | 0x4B000000u) - 8388608.0f, ms.y, ms.x);
+  for (int e = 0; e < 8; ++e) x[e] = fmaf(__uint_as_float(c[e]) - 8388608.0f, ms.y, ms.x);
   return pack16(x);
 }
+// Byte i of a word of single codes, as such a value.
+__device__ __forceinline__ uint32_t byte_value(uint32_t codes, int i) {
+  return __byte_perm(codes, 0x4B000000u, 0x7440 | i);
+}
+constexpr uint32_t kLow = 0x0F0F0F0Fu;
 
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kWarps * 32) paged_read_kernel(const ReadArgs a) {
@@ -488,17 +493,20 @@ __global__ void __launch_bounds__(kWarps * 32) paged_read_kernel(const ReadArgs 
     uint4 lo, hi;
     if (Q4) {
       uint32_t ca[8], cb[8];
+      if (is_k) {
+        const uint32_t a0 = code[t].x & kLow, a1 = (code[t].x >> 4) & kLow;
+        const uint32_t b0 = code[t].y & kLow, b1 = (code[t].y >> 4) & kLow;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (is_k) {
-          ca[e] = (code[t].x >> (4 * e)) & 0xFu;
-          cb[e] = (code[t].y >> (4 * e)) & 0xFu;
-        } else {
-          const uint32_t wa = e & 3 ? (e & 3) == 1 ? w[e / 4].y : (e & 3) == 2 ? w[e / 4].z : w[e / 4].w : w[e / 4].x;
-          const uint4& v = w[2 + e / 4];
-          const uint32_t wb = e & 3 ? (e & 3) == 1 ? v.y : (e & 3) == 2 ? v.z : v.w : v.x;
-          ca[e] = (wa >> (4 * t)) & 0xFu;
-          cb[e] = (wb >> (4 * t)) & 0xFu;
+        for (int e = 0; e < 8; ++e) {
+          ca[e] = byte_value(e & 1 ? a1 : a0, e / 2);
+          cb[e] = byte_value(e & 1 ? b1 : b0, e / 2);
+        }
+      } else {
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          ca[e] = ((words[e] >> (4 * t)) & 0xFu) | 0x4B000000u;
+          cb[e] = ((words[8 + e] >> (4 * t)) & 0xFu) | 0x4B000000u;
         }
       }
       lo = dequant_chunk(ca, __half22float2(*reinterpret_cast<const __half2*>(&ms[t].x)));
