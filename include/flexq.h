@@ -181,9 +181,10 @@ flexq_status flexq_linear_static_scratch(const void* x_dev, int ldx, const void*
  * x_dev fp16 [m][ldx] (ldx >= k, ldx % 8 == 0), residual_dev fp16 [m][ld_res],
  * y_dev fp16 [m][ldy], or fp32 with flag 8.  y may be residual (same
  * pointer and stride).  m == 0 does nothing; m > 16 returns
- * FLEXQ_ERR_UNSUPPORTED (flexq_linear takes it).  No workspace: the
+ * FLEXQ_ERR_UNSUPPORTED (flexq_linear takes it).  n <= 2^28, k <= 2^20.  No workspace: the
  * parts of a K axis that is shared out are joined inside the launch, in a fixed
- * order, so results do not depend on timing. */
+ * order, so results do not depend on timing.  A bounded wait that runs out is
+ * reported by flexq_device_status() (FLEXQ_ERR_TIMEOUT); y is then unspecified. */
 flexq_status flexq_gemv_q4(const void* x_dev, int ldx, const void* w_dev, int m, int n, int k,
                            const void* bias_dev, const void* residual_dev, int ld_res, int epilogue,
                            void* y_dev, int ldy, void* stream);
@@ -331,7 +332,9 @@ typedef struct {
  * not looked at.  A sequence that breaks a bound, a length below n_i, or a page
  * id outside the pool is reported by flexq_device_status() (FLEXQ_ERR_DEVICE);
  * nothing is read or written out of range, and what the call writes for that sequence
- * is unspecified. */
+ * is unspecified.  (A row_start that decreases somewhere leaves the other
+ * sequences unspecified too.)  Limits: b <= 65535, rows and max_len <= 2^24, rows *
+ * heads <= 2^30, b * kv_heads <= 2^24. */
 typedef struct {
   int b;
   int rows;
@@ -374,9 +377,17 @@ flexq_status flexq_paged_read(const flexq_config* cfg, const flexq_paged_kv* kv,
  * (append first): the row at position p attends over positions 0..p,
  * out[row][j*d ..] = softmax(q K^T / sqrt(d)) V with the cache's fp16
  * values (4-bit: the dequantized codes).  q_dev fp16 [rows][ldq], out_dev fp16
- * [rows][ldo].  Chunks of a prompt, single tokens, and both in one batch.  No
- * workspace: the parts of a long history that is shared out are joined inside
- * the launch, in a fixed order, so results do not depend on timing. */
+ * [rows][ldo], not over q.  Chunks of a prompt, single tokens, and both in one
+ * batch: sequences with up to 8 (or 16) query rows to a key/value head take a form that reads
+ * the cache at its bandwidth, the others one that multiplies on the tensor core's
+ * accumulator memory; a batch that may hold both is two launches.  Scores, the softmax's
+ * maximum and sum and the output are held in fp32; the weights enter the
+ * product with V in fp16, unnormalised.  Cached values below a sequence's
+ * kv_len must be finite (a later token's weight is zero, but zero times
+ * infinity is not); what slots at and behind kv_len hold does not matter.
+ * No workspace: the parts of a long history that is shared out are joined inside
+ * the launch, in a fixed order, so results do not depend on timing.  A bounded wait
+ * that runs out is reported as above. */
 flexq_status flexq_attention_paged(const flexq_config* cfg, const flexq_paged_kv* kv, const flexq_ragged* batch,
                                    const void* q_dev, int ldq, void* out_dev, int ldo, void* stream);
 

@@ -14,9 +14,10 @@
 //
 // Memory is the floor of both kernels: rows in, codes and pairs out, and for Q rows in and
 // out.  Measured (B200): 8345 rows of 8 key/value and 32 query heads, d = 128, rotated, to 4 bit:
-// 46 us for 175 MB (the quantizer's 28 instructions an element of K and V take half the issue
-// slots; prefetched rows, or more or fewer warps an SM, changed nothing); 2055 rows to fp16, d = 64: 12.5 us for
-// 51 MB; reading 19085 tokens of 32 heads back: 73 us for 401 MB, 0.84 of the copy rate (82 us with a
+// 43 us for 175 MB (rotation and quantization take half the issue slots; prefetched rows, or
+// more or fewer warps an SM, changed nothing; with a check of each code against the reciprocal's
+// error instead of the corrected quotient 46 us); 2055 rows to fp16, d = 64: 12.5 us for
+// 51 MB; reading 19085 tokens of 32 heads back: 68.5 us for 401 MB, 0.89 of the copy rate (82 us with a
 // lane's two chunks side by side, which its stores then half fill).
 //
 // The codes are exactly those of flexq_quantize on the (rotated) fp16 rows:
@@ -156,35 +157,27 @@ __device__ __forceinline__ Group group_of(uint32_t range) {
   return g;
 }
 
-// Codes of a chunk as the bits of 1.5 * 2^23 + code (0x4B400000 + code): adding that
-// number rounds to the nearest integer, half to even.  As in q64_code, the product with the
-// reciprocal stands in for the quotient wherever it is farther from a rounding boundary
-// than the two can differ (15 * 2^-20); within 2^-15 of one, which one chunk in some thousand
-// has, the chunk's quotients are computed.  x >= min, so codes are never negative;
-// a group whose scale was rounded down far (a subnormal one) needs the limit of 15.
+// Codes of a chunk, rint(a / s) of a = x - min, as the bits of 1.5 * 2^23 + code (0x4B400000 +
+// code): adding that number rounds to the nearest integer, half to even.  The quotient is the
+// correctly rounded one without a division, by the correction step of fifteenth(): with y the rounded
+// reciprocal, q + (a - q s) y is within 1.5 ulp * 2^-24 of a / s.  A midpoint of two fp32 numbers
+// has 25 bits and s has 11, so a / s, unless it is one, is at least 2^-11 of half an ulp away from every
+// midpoint; and it never is one, since the product of an odd 25-bit number with s does not fit a's
+// 24 bits.  x >= min, so codes are never negative; only a subnormal scale can have been rounded down
+// so far that a quotient exceeds 15.5.
 constexpr uint32_t kCodeBias = 0x4B400000u;
-__device__ __noinline__ void exact_codes(uint4 raw, float mn, float sc, uint32_t* c) {
-  float x[8];
-  unpack(raw, x);
-#pragma unroll 1
-  for (int e = 0; e < 8; ++e)
-    c[e] = __float_as_uint(__fadd_rn(fminf(__fdiv_rn(__fsub_rn(x[e], mn), sc), 15.0f), 12582912.0f));
-}
 __device__ __forceinline__ void chunk_codes(const uint4& raw, const Group& g, uint32_t (&c)[8]) {
-  float x[8], far = 0.0f;
+  float x[8];
   unpack(raw, x);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float r = fminf(__fmul_rn(__fsub_rn(x[e], g.mn), g.inv), 15.0f);
-    const float k = __fadd_rn(r, 12582912.0f);
-    c[e] = __float_as_uint(k);
-    far = fmaxf(far, fabsf(__fsub_rn(r, __fsub_rn(k, 12582912.0f))));
+    const float d = __fsub_rn(x[e], g.mn);
+    const float q = __fmul_rn(d, g.inv);
+    c[e] = __float_as_uint(__fadd_rn(fmaf(fmaf(-g.sc, q, d), g.inv, q), 12582912.0f));
   }
-  if (far >= 0.5f - 0x1p-15f && g.sc != 0.0f) {
-    uint32_t exact[8];
-    exact_codes(raw, g.mn, g.sc, exact);
+  if (g.sc < 0x1p-14f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = exact[e];
+    for (int e = 0; e < 8; ++e) c[e] = min(c[e], kCodeBias + 15);
   }
 }
 
@@ -353,6 +346,7 @@ __global__ void __launch_bounds__(kWarps * 32, 6) paged_append_kernel(const Appe
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) w[e] = 0u;
+  uint32_t places = 0;  // of the tokens in the words: the codes' biases come off at the end
   constexpr int B = Q4 ? 1 : 2;  // tokens in flight (4-bit: more warps instead, by the registers)
   for (int t = un.t0; t < un.t1; t += B) {
     uint4 ra[B], rb[B];
@@ -392,17 +386,20 @@ __global__ void __launch_bounds__(kWarps * 32, 6) paged_append_kernel(const Appe
           *reinterpret_cast<uint32_t*>(dst + sl.eb / 2) = pack_codes(cb);
         }
       } else {
-        const int sh = 4 * (t + i - base);
+        const uint32_t place = 1u << (4 * (t + i - base));
+        places += place;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          w[e] += (ca[e] - kCodeBias) << sh;
-          w[8 + e] += (cb[e] - kCodeBias) << sh;
+          w[e] += ca[e] * place;
+          w[8 + e] += cb[e] * place;
         }
       }
     }
   }
   if (Q4 && kind == kV && live) {
     const uint32_t kept = ~static_cast<uint32_t>(((1ull << (4 * (un.t1 - un.t0))) - 1) << (4 * (un.t0 - base)));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] -= places * kCodeBias;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       *word4(q) = make_uint4(w[4 * q] | (old[q].x & kept), w[4 * q + 1] | (old[q].y & kept),

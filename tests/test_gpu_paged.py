@@ -9,7 +9,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 import paged_helpers as ph  # noqa: E402
-from gpu_helpers import fq, to_dev, to_host  # noqa: E402
+from gpu_helpers import f16_groups, fq, to_dev, to_host  # noqa: E402
 
 
 class Dev:
@@ -125,6 +125,29 @@ def test_append_special_values_follow_the_codec():
     for r, x in enumerate(rows):
         k[r, 64:128], v[r, 0:64] = x.astype(np.float16), x.astype(np.float16)
     fq.flexq_paged_append(dv.cfg, dv.kv, dv.batch, None, to_dev(k), to_dev(v), 256)
+    fq.flexq_device_status()
+    for got, want in zip((dv.k, dv.v, dv.km, dv.vm), ph.append_reference(pg, k, v)[0]):
+        same_bits(to_host(got), want)
+
+
+@pytest.mark.parametrize("d,kv_heads", [(128, 4), (64, 6)])
+def test_append_codes_at_every_magnitude_and_next_to_rounding_boundaries(d, kv_heads):
+    """Groups of 1e-6 to 1e4 with the codec's special ones, subnormal scales, and groups whose
+    elements sit on, just below and just above code + 1/2 steps of their scale."""
+    n = 700
+    pg = ph.Paged(4, kv_heads, kv_heads, d, 64, (n,), (3,), seed=12)
+    dv = Dev(pg)
+    rng = np.random.default_rng(5)
+    width = kv_heads * d
+    k = f16_groups(rng, n * width // 64).reshape(n, width)
+    sc = rng.integers(1, 0x6000, n * width // 64).astype(np.uint16).view(np.float16).astype(np.float64)[:, None]
+    lo = rng.choice([0.0, -7.5, 3.0, -15.0], (len(sc), 1)) * sc
+    x = (lo + (rng.integers(0, 16, (len(sc), 64)) + rng.choice([0.0, 0.5], (len(sc), 64))) * sc)
+    x[:, 0], x[:, 1] = lo[:, 0], lo[:, 0] + 15 * sc[:, 0]
+    x = np.clip(x, -32768, 32768).astype(np.float16)
+    nudge = rng.integers(-2, 3, x.shape).astype(np.int16) * (np.abs(x) > 1e-6) * (np.abs(x) < 3e4)
+    v = np.ascontiguousarray((x.view(np.int16) + nudge.astype(np.int16)).view(np.float16)).reshape(n, width)
+    fq.flexq_paged_append(dv.cfg, dv.kv, dv.batch, None, to_dev(k), to_dev(v), width)
     fq.flexq_device_status()
     for got, want in zip((dv.k, dv.v, dv.km, dv.vm), ph.append_reference(pg, k, v)[0]):
         same_bits(to_host(got), want)
