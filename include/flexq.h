@@ -180,7 +180,7 @@ flexq_status flexq_linear_static_scratch(const void* x_dev, int ldx, const void*
  * flexq_linear's epilogue flags; the two differ only in the order of the sums.
  * x_dev fp16 [m][ldx] (ldx >= k, ldx % 8 == 0), residual_dev fp16 [m][ld_res],
  * y_dev fp16 [m][ldy], or fp32 with flag 8.  y may be residual (same
- * pointer and stride).  m == 0 does nothing; m > 16 returns
+ * pointer and stride), but not overlap x.  m == 0 does nothing; m > 16 returns
  * FLEXQ_ERR_UNSUPPORTED (flexq_linear takes it).  n <= 2^28, k <= 2^20.  No workspace: the
  * parts of a K axis that is shared out are joined inside the launch, in a fixed
  * order, so results do not depend on timing.  A bounded wait that runs out is
@@ -384,7 +384,8 @@ flexq_status flexq_paged_read(const flexq_config* cfg, const flexq_paged_kv* kv,
  * maximum and sum and the output are held in fp32; the weights enter the
  * product with V in fp16, unnormalised.  Cached values below a sequence's
  * kv_len must be finite (a later token's weight is zero, but zero times
- * infinity is not); what slots at and behind kv_len hold does not matter.
+ * infinity is not), and scores q k / sqrt(d) below 2^22 in magnitude; what slots at and
+ * behind kv_len hold does not matter.
  * No workspace: the parts of a long history that is shared out are joined inside
  * the launch, in a fixed order, so results do not depend on timing.  A bounded wait
  * that runs out is reported as above. */

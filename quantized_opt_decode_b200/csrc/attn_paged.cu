@@ -499,21 +499,44 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
   cluster.sync();  // nobody leaves while another reads its shared memory
 }
 
+// How a unit's history is dealt out: warps of a CTA and CTAs of a cluster (its tiles go round
+// them all).  An SM holds 16 warps.  Very many units: two warps each, so that the fixed cost of a
+// unit is shared by few (8064 units of 300 to 1040 keys: 205 us with two, 211 with four, 231 with one).  Few
+// units: the largest number of warps that is resident at once.  Where that leaves a fifth of the SMs'
+// room empty and histories are long, four-warp CTAs in at least two and a half rounds, down to
+// 512 keys a CTA (320 units of 8000 keys: 118 us in one round of 320 CTAs).
+struct Plan {
+  int warps, splits;
+};
+Plan plan_rows(long long units, int max_len, int tile, int sms) {
+  if (units >= 32ll * sms) return {2, 1};
+  const long long tiles = (max_len + tile - 1) / tile;
+  Plan best{4, 1};
+  long long resident = 0;
+  for (const int warps : {4, 8}) {
+    if (warps > 4 && tiles < warps) continue;
+    const long long room = 16 / warps * sms;  // CTAs at once
+    const long long splits = std::min({static_cast<long long>(kMaxCluster), room / units, std::max(1ll, tiles / warps)});
+    if (splits >= 1 && units * splits * warps > resident) {
+      resident = units * splits * warps;
+      best = {warps, static_cast<int>(splits)};
+    }
+  }
+  if (resident >= 13ll * sms) return best;
+  const long long rounds = (10ll * sms + units - 1) / units;  // splits for 2.5 rounds of 4 CTAs an SM
+  const long long splits = std::min({static_cast<long long>(kMaxCluster), rounds, static_cast<long long>(max_len / 512)});
+  return splits > 1 && units * splits >= 5ll * sms ? Plan{4, static_cast<int>(splits)} : best;
+}
+
 template <int D, bool Q4, int NT>
 cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   using T = Tile<D, Q4>;
   static_assert(T::stages * T::bytes >= 8 * NT * D * 4, "a warp's ring holds its partial output");
   cudaError_t e = allow_smem<attn_paged_rows_kernel<D, Q4, NT>>(kMaxWarps * T::stages * T::bytes);
   if (e != cudaSuccess) return e;
-  // Warps of a unit (its tiles go round them): what 16 warps an SM give it, but no more
-  // than it has tiles; four or, with very many units, two at the least, so that the fixed
-  // cost of a unit stays small (8064 units of 300 to 1040 keys: 205 us with two, 211 with four, 231
-  // with one).
+  const Plan plan = plan_rows(static_cast<long long>(a.batch.b) * a.kv.kv_heads, a.batch.max_len, T::keys, runtime().num_sms);
+  const int warps = plan.warps, splits = plan.splits;
   const long long units = static_cast<long long>(a.batch.b) * a.kv.kv_heads;
-  const long long tiles = (a.batch.max_len + T::keys - 1) / T::keys;
-  const long long ways = std::min(16ll * runtime().num_sms / units, tiles);
-  const int warps = ways >= 8 ? 8 : ways >= 4 || 2 * units < 64ll * runtime().num_sms ? 4 : 2;
-  const int splits = static_cast<int>(std::max(1ll, std::min<long long>(kMaxCluster, ways / warps)));
   const int smem = warps * T::stages * T::bytes;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
