@@ -509,8 +509,9 @@ struct Plan {
   int warps, splits;
 };
 Plan plan_rows(long long units, int max_len, int tile, int sms) {
-  if (units >= 32ll * sms) return {2, 1};
   const long long tiles = (max_len + tile - 1) / tile;
+  if (tiles <= 2) return {static_cast<int>(tiles), 1};  // no warp without a tile
+  if (units >= 32ll * sms) return {2, 1};
   Plan best{4, 1};
   long long resident = 0;
   for (const int warps : {4, 8}) {
