@@ -39,8 +39,10 @@
 // same sizes: scores of 64 keys, twice, so that the next are there when a softmax ends (464 us: twice
 // the hand-offs); one thread a row tile issuing the products (547 us against 451: both softmaxes
 // then run at the same time); a quarter of the exponentials as polynomials (446 us: issue slots);
-// loops rolled up for the instruction cache (519 us); four loading warps (446 us).  The roles'
-// waits are inlined: a function call would tie the roles to one register count.
+// loops rolled up for the instruction cache (519 us); four loading warps (446 us); the largest score of the
+// whole tile first, P then handed over in halves (447 us: scores are read twice); two key tiles at once
+// for units of one row tile (434 us); pages' entries looked at a step after their load (423 us).  The
+// roles' waits are inlined: a function call would tie the roles to one register count.
 #include <cooperative_groups.h>
 #include <math.h>
 
