@@ -16,7 +16,8 @@
 // 41 us for 119 MB; one row, 2048 x 2048: 5.0 us, the launch.  Bound by the half-precision pipe that the
 // dequantizer's multiply-adds and mma.sync share (190 of the 290 cycles that four warps take
 // for a k-block), and by 224 tiles on 148 SMs: two on some, one on others; sharing K out more finely cost
-// more than it evened out (38 us with two parts, 51 with eight).  Tried: a warp a K slice with its own ring of
+// more than it evened out (38 us with two parts, 51 with eight), and so did CTAs of 64 or 32 features
+// (41 and 44 us; 53 and 51 for the larger).  Tried: a warp a K slice with its own ring of
 // 16-byte copies (41 and 50 us: 600 instructions for 2304 bytes, half of them addresses and copies
 // of X); X through the L1 cache (36 and 47 us); the dequantized rows in tensor memory and the products on
 // tcgen05 (42 and 38 us, 6.3 instead of 5.0 us for the small one: the hand-offs between the
