@@ -47,6 +47,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "paged.cuh"
 #include "warp_mma.cuh"
@@ -285,9 +286,9 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
   return static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
 }
 
-// One key tile of a unit; t < 0: none.
+// One key tile of a unit, the CTA's u-th; t < 0: none.
 struct TileRef {
-  int i, head, t, len;
+  int i, head, t, len, u;
 };
 
 // What a loading lane holds of one tile: its part of up to two 8-token blocks.
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   const int lane = static_cast<int>(lane_id());
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
   const int g = a.group;
-  // With a history shared out over a cluster, a cluster has one unit number.
+  // With a history shared out over a cluster, the cluster's CTAs walk the same units.
   UnitWalk walk;
   Unit un;
   walk.start(a, blockIdx.x / splits, gridDim.x / splits);
@@ -508,6 +509,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   };
   // key tiles of this CTA: rank, rank + splits, ..
   auto tiles_of = [&](const Unit& x) { return x.tiles > rank ? (x.tiles - rank + splits - 1) / splits : 0; };
+  // A shared-out unit ends with two barriers of the whole cluster, which every warp passes whatever
+  // became of its waits: parts are written before the first and read before the second.  No wait of a
+  // role falls between them, so all see the same failures and leave together.
+  auto cluster_sync = [&]() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  auto cluster_fine = [&]() {
+    bool fine = true;
+#pragma unroll 1
+    for (int k = 0; k < splits; ++k) fine &= *cluster.map_shared_rank(&s_fail, k) == 0;
+    return __all_sync(0xffffffffu, fine) != 0;
+  };
+  auto unit_end = [&]() {  // (false: no further unit)
+    cluster_sync();
+    const bool fine = cluster_fine();
+    cluster_sync();
+    return fine;
+  };
 
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -537,15 +558,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       if (lane == 0) mbar_arrive(&bar.q_full[m]);
     };
     bool more = true, ok = true;
-    while (more && m * 128 >= un.rows) more = walk.next(a, un);  // row tile 1: units that have one
-    if (more) load_q(un);
-    uint32_t s_phase = 0, o_phase = 0;
+    // row tile 1: units that have one (of a shared-out unit, the join alone)
+    while (more && splits == 1 && m * 128 >= un.rows) more = walk.next(a, un);
+    if (more && m * 128 < un.rows) load_q(un);
+    uint32_t s_phase = 0, o_phase = 0;  // o_phase: bit m row tile m's
     while (more) {
       const Unit cur = un;
+      const bool has = m * 128 < cur.rows;
       const bool live = row < cur.rows;
       const int c = cur.c0 + (live ? row : 0), tok = c / g;
       const int pos = live ? cur.first + tok : cur.len;
-      const int mine = tiles_of(cur);
+      const int mine = has ? tiles_of(cur) : 0;
       float base = -INFINITY;   // exponent base: log2 of the weights' unit, a whole number
       float limit = -INFINITY;  // the raw score that moves it
       uint64_t sum = 0;        // sums of the even and the odd columns' weights
@@ -639,20 +662,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[m]);
       }
-      if (!ok) break;
-      do more = walk.next(a, un);
-      while (more && m * 128 >= un.rows);
-      if (more) load_q(un);
-
-      ok = __all_sync(0xffffffffu, wait(&bar.o_full[m], o_phase, DEV_TIMEOUT_EPILOGUE));
-      if (ok && splits > 1 && cur.rows > 128)  // the parts are laid over K and V: wait for both row tiles
-        ok = __all_sync(0xffffffffu, wait(&bar.o_full[m ^ 1], 0, DEV_TIMEOUT_EPILOGUE));
-      if (!ok) break;
-      o_phase ^= 1;
-      tc_fence_after();
       float s0, s1;
       unpair(sum, s0, s1);
       if (splits == 1) {
+        if (!ok) break;
+        do more = walk.next(a, un);
+        while (more && m * 128 >= un.rows);
+        if (more) load_q(un);
+
+        if (!(ok = __all_sync(0xffffffffu, wait(&bar.o_full[m], (o_phase >> m) & 1, DEV_TIMEOUT_EPILOGUE)))) break;
+        tc_fence_after();
         const float inv = 1.f / (s0 + s1);
         __half* dst = a.out + static_cast<size_t>(cur.row0 + tok) * a.ldo + (cur.head * g + c - tok * g) * D;
 #pragma unroll 1
@@ -676,23 +695,71 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.o_free[m]);
       } else {
-        s_m[row] = base;
-        s_l[row] = s0 + s1;
-        // in O's column order, 16-byte units XORed by the row
+        if (ok && has) ok = __all_sync(0xffffffffu, wait(&bar.o_full[m], (o_phase >> m) & 1, DEV_TIMEOUT_EPILOGUE));
+        if (ok && has && cur.rows > 128)  // the parts are laid over K and V: wait for both row tiles
+          ok = __all_sync(0xffffffffu, wait(&bar.o_full[m ^ 1], (o_phase >> (m ^ 1)) & 1, DEV_TIMEOUT_EPILOGUE));
+        if (ok && has) {
+          tc_fence_after();
+          s_m[row] = base;
+          s_l[row] = s0 + s1;
+          // in O's column order, 16-byte units XORed by the row
 #pragma unroll 1
-        for (int q = 0; q < D; q += 8) {
-          uint32_t o[8];
-          if (mine > 0) {
-            tmem_read_x8(o_col + q, o);
-          } else {
+          for (int q = 0; q < D; q += 8) {
+            uint32_t o[8];
+            if (mine > 0) {
+              tmem_read_x8(o_col + q, o);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0u;
+              for (int e = 0; e < 8; ++e) o[e] = 0u;
+            }
+            const uint32_t at = sbase + L::k0 + row * (D * 4);
+            sts128(at + (((q >> 2) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+            sts128(at + ((((q >> 2) + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
           }
-          const uint32_t at = sbase + L::k0 + row * (D * 4);
-          sts128(at + (((q >> 2) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-          sts128(at + ((((q >> 2) + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && mine > 0) mbar_arrive(&bar.o_free[m]);
         }
+        cluster_sync();
+        const bool fine = cluster_fine();
+        // join the cluster's parts: CTA `rank` takes every splits-th group of four columns
+        constexpr int C4 = D / 4;
+        // (an aligned base is at the same offset in every CTA of the launch)
+        const float4* parts = reinterpret_cast<const float4*>(smem + L::k0);
+        for (int x = rank * (kSoftmaxWarps * 32) + threadIdx.x; fine && x < cur.rows * C4; x += splits * (kSoftmaxWarps * 32)) {
+          const int jr = x / C4, c4 = x % C4;
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int k = 0; k < splits; ++k) top = fmaxf(top, *cluster.map_shared_rank(&s_m[jr], k));
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float den = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < splits; ++k) {
+            const float mk = *cluster.map_shared_rank(&s_m[jr], k);
+            const float4 pk = *cluster.map_shared_rank(parts + jr * C4 + (c4 ^ (jr & 7)), k);
+            const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - top);
+            den += f * *cluster.map_shared_rank(&s_l[jr], k);
+            acc.x += f * pk.x;
+            acc.y += f * pk.y;
+            acc.z += f * pk.z;
+            acc.w += f * pk.w;
+          }
+          const float inv = 1.f / den;
+          const int jc = cur.c0 + jr;
+          __half* dst = a.out + static_cast<size_t>(cur.row0 + jc / g) * a.ldo + (cur.head * g + jc % g) * D;
+          const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = c4 * 4 + e;
+            dst[W * (col % (D / W)) + col / (D / W)] = __float2half_rn(o[e]);
+          }
+        }
+        cluster_sync();  // nobody writes, or leaves, while another reads its shared memory
+        if (!fine) break;
+        more = walk.next(a, un);
+        if (more && m * 128 < un.rows) load_q(un);
       }
+      o_phase ^= cur.rows > 128 ? 3u : 1u;
     }
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
@@ -703,14 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     ld.lane = lane;
     ld.sub = lane % Ld::lanes;
     bool more = true;
-    int it = 0, mine = tiles_of(un);
+    int it = 0, mine = tiles_of(un), units = 0;
     auto advance = [&]() {  // the CTA's next tile
       while (more && it == mine) {
         more = walk.next(a, un);
         it = 0;
         mine = more ? tiles_of(un) : 0;
+        ++units;
       }
-      TileRef x{un.i, un.head, -1, un.len};
+      TileRef x{un.i, un.head, -1, un.len, units};
       if (more) x.t = rank + it++ * splits;
       return x;
     };
@@ -720,11 +788,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     ld.look_up(a, next, next_page);
     if constexpr (Q4) ld.fetch_k(a, cur, page);
     if constexpr (Q4) ld.fetch_v(a, cur, page);
+    int ended = 0;  // shared-out units behind this warp
+    bool fine = true;
+    auto end_units = [&](int count) {
+      for (; splits > 1 && fine && ended < count; ++ended) fine = unit_end();
+    };
     for (int n = 0; cur.t >= 0; ++n) {
+      end_units(cur.u);  // (their parts lie over the stages)
+      if (!fine) break;
       const int st = n % kStages;
       const uint32_t free_parity = ((n / kStages) & 1) ^ 1;
       const uint32_t ks = sbase + L::k0 + st * L::k_stage, vs = sbase + L::v0 + st * L::v_stage;
-      if (!__all_sync(0xffffffffu, wait(&bar.k_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
+      if (!__all_sync(0xffffffffu, wait(&bar.k_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) {
+        units = cur.u + 1;
+        break;
+      }
       if constexpr (Q4) {
         ld.store_k(ks);
       } else {
@@ -736,7 +814,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.k_full[st]);
       if constexpr (Q4) ld.fetch_k(a, next, next_page);
-      if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) break;
+      if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) {
+        units = cur.u + 1;
+        break;
+      }
       ld.store_v(vs);
       fence_proxy_async_smem();
       __syncwarp();
@@ -748,6 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       for (int q = 0; q < Ld::NQ; ++q) page[q] = next_page[q];
       ld.look_up(a, next, next_page);
     }
+    end_units(units);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     if (warp == kMmaWarp) {
@@ -809,7 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         q_phase ^= used;
         if (mine > 0) o_phase ^= used;
         if (mine & 1) p_phase ^= used;
-        if (ok) more = walk.next(a, un);
+        if (splits > 1) more = unit_end();  // (not ok: nor is it fine)
+        if (ok && more) more = walk.next(a, un);
       }
       __syncwarp();
       if (elect_one()) {
@@ -818,6 +901,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         // them, whatever the waits' limit
         if (!wait_phase(&bar.done, 0, kDrainNs)) set_error(a.err, DEV_TIMEOUT_MMA);
       }
+    } else {
+      for (bool more = splits > 1; more;) more = unit_end() && walk.next(a, un);
     }
   }
   __syncwarp();
@@ -825,48 +910,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   __syncthreads();
   pdl_trigger();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-  if (splits == 1) return;
-
-  // join the cluster's parts: CTA `rank` takes every splits-th group of four columns
-  cluster.sync();
-  bool fine = true;
-  for (int k = 0; k < splits; ++k) fine &= *cluster.map_shared_rank(&s_fail, k) == 0;
-  constexpr int C4 = D / 4;
-  walk.start(a, blockIdx.x / splits, gridDim.x / splits);  // the cluster's one unit again
-  walk.next(a, un);
-  const int rows = un.rows;
-  // (an aligned base is at the same offset in every CTA of the launch)
-  const float4* parts = reinterpret_cast<const float4*>(smem + L::k0);
-  for (int x = rank * kThreads + threadIdx.x; fine && x < rows * C4; x += splits * kThreads) {
-    const int row = x / C4, c4 = x % C4;
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int k = 0; k < splits; ++k) top = fmaxf(top, *cluster.map_shared_rank(&s_m[row], k));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f;
-#pragma unroll 1
-    for (int k = 0; k < splits; ++k) {
-      const float mk = *cluster.map_shared_rank(&s_m[row], k);
-      const float4 pk = *cluster.map_shared_rank(parts + row * C4 + (c4 ^ (row & 7)), k);
-      const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - top);
-      den += f * *cluster.map_shared_rank(&s_l[row], k);
-      acc.x += f * pk.x;
-      acc.y += f * pk.y;
-      acc.z += f * pk.z;
-      acc.w += f * pk.w;
-    }
-    const float inv = 1.f / den;
-    const int c = un.c0 + row;
-    __half* dst = a.out + static_cast<size_t>(un.row0 + c / g) * a.ldo + (un.head * g + c % g) * D;
-    const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int col = c4 * 4 + e;
-      dst[W * (col % (D / W)) + col / (D / W)] = __float2half_rn(o[e]);
-    }
-  }
-  __syncwarp();
-  cluster.sync();  // nobody leaves while another reads its shared memory
 }
 
 template <int D, bool Q4>
@@ -892,7 +935,7 @@ cudaError_t launch_d(const ChunkArgs& a, cudaStream_t s) {
   if (full < 4ll * sms)
     splits = std::max(splits, std::min(kMaxCluster, a.batch.max_len / (32 * kKeys)));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? works * splits : std::min<long long>(works, sms)));
+  cfg.gridDim = dim3(static_cast<unsigned>(splits));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Layout<D>::smem;
   cfg.stream = s;
@@ -904,6 +947,15 @@ cudaError_t launch_d(const ChunkArgs& a, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = runtime().pdl ? 2 : 1;
+  // one CTA an SM, or as many clusters as are resident at once
+  static std::atomic<int> resident[kMaxCluster + 1];
+  int clusters = splits == 1 ? sms : resident[splits].load(std::memory_order_relaxed);
+  if (clusters == 0) {
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, attn_paged_chunk_kernel<D, Q4>, &cfg)) != cudaSuccess) return e;
+    clusters = std::max(clusters, 1);
+    resident[splits].store(clusters, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(works, clusters) * splits));
   e = cudaLaunchKernelEx(&cfg, attn_paged_chunk_kernel<D, Q4>, a);
   return e != cudaSuccess ? e : launched();
 }

@@ -282,6 +282,27 @@ def test_loose_bounds_give_the_same_rows(max_new, max_len):
     check_attention(pg, q, to_host(out), k=pools[0], v=pools[1], km=pools[2], vm=pools[3])
 
 
+@pytest.mark.parametrize("bits,heads,kv_heads,d", [(4, 16, 8, 128), (4, 12, 12, 64), (16, 8, 8, 128)])
+def test_short_units_under_the_bound_of_a_very_long_one(bits, heads, kv_heads, d):
+    """A cluster then shares out each of the several units it has, most with fewer tiles than CTAs:
+    units of one and two row tiles, empty and single-token sequences between them."""
+    new = (300, 1, 20, 0, 140, 64, 1, 9, 260, 100)
+    past = (0, 40, 900, 7, 500, 0, 1300, 3000, 70, 260)
+    pg = ph.Paged(bits, heads, kv_heads, d, 128, new, past, seed=heads, front=2, pad=9)
+    pg.table = np.concatenate([pg.table, np.full((pg.b, 256), -1, np.int32)], 1)
+    pg.table_ld = pg.table.shape[1]
+    dv = Dev(pg, max_len=256 * 128)
+    q = pg.new_rows()[2]
+    qd = to_dev(q)
+    outs = [torch.full((pg.rows, heads * d), float("nan"), dtype=torch.float16, device="cuda") for _ in range(3)]
+    for out in outs:
+        fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, qd, heads * d, out, heads * d)
+    fq.flexq_device_status()
+    check_attention(pg, q, to_host(outs[0]))
+    for out in outs[1:]:
+        same_bits(to_host(out), to_host(outs[0]))
+
+
 def test_many_sequences():
     """More sequences than one probe round of the owner search covers."""
     rng = np.random.default_rng(0)

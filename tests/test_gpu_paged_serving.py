@@ -245,16 +245,20 @@ def test_two_streams_at_once():
         same_bits(to_host(job[8]), y)
 
 
-@pytest.mark.parametrize("op", ["product", "chunks", "chunks of a shared-out history"])
+@pytest.mark.parametrize("op", ["product", "chunks", "chunks of a shared-out history", "many shared-out units"])
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(op):
     if op == "product":
         x, w, bias, res, wq, _ = gemv_case(5, 640, 4096, 0)
         xd, out = to_dev(x), torch.empty(5, 640, dtype=torch.float16, device="cuda")
         run = lambda: fq.flexq_gemv_q4(xd, 4096, wq, 5, 640, 4096, None, None, 0, 0, out, 640)  # noqa: E731
     else:
-        new, past = ((300, 150), (100, 20)) if op == "chunks" else ((20,), (6000,))
+        new, past = {"chunks": ((300, 150), (100, 20)), "many shared-out units": ((40,) * 30, (200,) * 30)}.get(
+            op, ((20,), (6000,)))
         pg = ph.Paged(4, 2, 2, 128, 32, new, past, seed=2)
-        dv = Dev(pg)
+        if op == "many shared-out units":
+            pg.table = np.concatenate([pg.table, np.full((pg.b, 1024), -1, np.int32)], 1)
+            pg.table_ld = pg.table.shape[1]
+        dv = Dev(pg, max_len=32768 if op == "many shared-out units" else None)
         q = pg.new_rows()[2]
         qd, out = to_dev(q), torch.empty(pg.rows, 256, dtype=torch.float16, device="cuda")
         run = lambda: fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, qd, 256, out, 256)  # noqa: E731
