@@ -77,6 +77,7 @@ struct ChunkArgs {
   RaggedView batch;
   int heads, group;
   int min_rows;
+  int joint_tiles;  // tiles from which on a unit is shared out
   const __half* q;
   int ldq;
   __half* out;
@@ -107,29 +108,42 @@ struct Barriers {
 // 256 query rows of one sequence and key/value head.
 struct Unit {
   int i, head, row0, first, len, c0, rows;
-  int tiles;  // key tiles that some row of the unit sees
+  int tiles;   // key tiles that some row of the unit sees
+  bool joint;  // shared out over the cluster
 };
 
-// The units of CTA (or cluster) `id` of `count`, in order: one of each `count` unit
+// The units of CTA (or cluster) `id` of `stride`, in order: one of each `stride` unit
 // numbers, from the front and from the back by turns (long units tend to come first), 32 looked
-// up at a time, one by each lane; those that hold no rows are passed over.
+// up at a time, one by each lane; those that hold no rows are passed over.  In a launch of clusters
+// first the cluster's, of joint_tiles tiles and more, then the CTA's own, the shorter ones: a
+// bound on lengths far above the batch's costs a search.
+template <bool J>
 struct UnitWalk {
   long long round, total;
   int id, stride;
+  bool joint;
   uint32_t found;
   int i, head, row0, n, len, c0;
 
-  __device__ __forceinline__ void start(const ChunkArgs& a, int id_, int count) {
+  __device__ __forceinline__ void start(const ChunkArgs& a, int splits) {
     total = unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1) * a.kv.kv_heads;
-    id = id_;
-    stride = count;
+    joint = J;
+    id = static_cast<int>(blockIdx.x) / splits;
+    stride = static_cast<int>(gridDim.x) / splits;
     round = 0;
     found = 0;
   }
   // Every lane of the warp calls this and gets the same unit; false: no more.
   __device__ __forceinline__ bool next(const ChunkArgs& a, Unit& out) {
     while (found == 0) {
-      if (round * stride >= total) return false;
+      if (round * stride >= total) {
+        if (!J || !joint) return false;
+        joint = false;
+        id = static_cast<int>(blockIdx.x);
+        stride = static_cast<int>(gridDim.x);
+        round = 0;
+        continue;
+      }
       const long long k = round + lane_id();
       const long long w = k * stride + (k & 1 ? stride - 1 - id : id);
       round += 32;
@@ -146,7 +160,8 @@ struct UnitWalk {
     const int tokens = __shfl_sync(0xffffffffu, n, from);
     out.first = out.len - tokens;
     out.rows = min(kRows, tokens * g - out.c0);
-    out.tiles = (out.first + (out.c0 + out.rows - 1) / g + kKeys) / kKeys;
+    out.tiles = tiles_of(out.first, out.c0, out.rows, g);
+    out.joint = J && joint;
     return true;
   }
   __device__ __forceinline__ bool look(const ChunkArgs& a, int w) {
@@ -166,7 +181,11 @@ struct UnitWalk {
     const int rel = u - static_cast<int>(unit_base(a.batch, i, g, kRowShift, 1));
     const int units = (rows + kRows - 1) / kRows;
     c0 = (units - 1 - rel) * kRows;  // the later rows, which see more keys, first
-    return sp.n > 0 && rows >= a.min_rows && rel >= 0 && rel < units;
+    return sp.n > 0 && rows >= a.min_rows && rel >= 0 && rel < units &&
+           (!J || (tiles_of(len - n, c0, min(kRows, rows - c0), g) >= a.joint_tiles) == joint);
+  }
+  static __device__ __forceinline__ int tiles_of(int first, int c0, int rows, int g) {
+    return (first + (c0 + rows - 1) / g + kKeys) / kKeys;
   }
 };
 
@@ -286,9 +305,9 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
   return static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
 }
 
-// One key tile of a unit, the CTA's u-th; t < 0: none.
+// One key tile of a unit; t < 0: none.  `before`, `with`: shared-out units before its unit, and with it.
 struct TileRef {
-  int i, head, t, len, u;
+  int i, head, t, len, before, with;
 };
 
 // What a loading lane holds of one tile: its part of up to two 8-token blocks.
@@ -451,7 +470,8 @@ struct Loader<D, false> {
   }
 };
 
-template <int D, bool Q4>
+// J: in clusters, which share out long units.
+template <int D, bool Q4, bool J>
 __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const ChunkArgs a) {
   using L = Layout<D>;
   constexpr int W = Q4 ? 4 : 8;  // O's column (D / W) e + u is dimension W u + e
@@ -461,17 +481,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   __shared__ int s_fail;
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
-  const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int splits = J ? static_cast<int>(cluster.num_blocks()) : 1, rank = J ? static_cast<int>(cluster.block_rank()) : 0;
   const int lane = static_cast<int>(lane_id());
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
   const int g = a.group;
-  // With a history shared out over a cluster, the cluster's CTAs walk the same units.
-  UnitWalk walk;
+  UnitWalk<J> walk;
   Unit un;
-  walk.start(a, blockIdx.x / splits, gridDim.x / splits);
+  walk.start(a, splits);
   const bool any = walk.next(a, un);
   if (blockIdx.x == 0 && warp == kMmaWarp + 1) check_spans(a.batch, a.err);
-  if (!any) return;  // (every warp of the cluster alike)
+  if (!any) return;  // (every warp of the CTA alike; of the cluster, if it has a shared-out unit)
 
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
@@ -507,8 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     atomicExch(&s_fail, 1);
     return false;
   };
-  // key tiles of this CTA: rank, rank + splits, ..
-  auto tiles_of = [&](const Unit& x) { return x.tiles > rank ? (x.tiles - rank + splits - 1) / splits : 0; };
+  // key tiles of this CTA: all, or rank, rank + splits, ..
+  auto first_of = [&](const Unit& x) { return J && x.joint ? rank : 0; };
+  auto step_of = [&](const Unit& x) { return J && x.joint ? splits : 1; };
+  auto tiles_of = [&](const Unit& x) {
+    return !J || !x.joint ? x.tiles : x.tiles > rank ? (x.tiles - rank + splits - 1) / splits : 0;
+  };
   // A shared-out unit ends with two barriers of the whole cluster, which every warp passes whatever
   // became of its waits: parts are written before the first and read before the second.  No wait of a
   // role falls between them, so all see the same failures and leave together.
@@ -559,12 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     };
     bool more = true, ok = true;
     // row tile 1: units that have one (of a shared-out unit, the join alone)
-    while (more && splits == 1 && m * 128 >= un.rows) more = walk.next(a, un);
+    while (more && !(J && un.joint) && m * 128 >= un.rows) more = walk.next(a, un);
     if (more && m * 128 < un.rows) load_q(un);
     uint32_t s_phase = 0, o_phase = 0;  // o_phase: bit m row tile m's
     while (more) {
       const Unit cur = un;
-      const bool has = m * 128 < cur.rows;
+      const bool has = !J || m * 128 < cur.rows;
       const bool live = row < cur.rows;
       const int c = cur.c0 + (live ? row : 0), tok = c / g;
       const int pos = live ? cur.first + tok : cur.len;
@@ -576,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         if (!(ok = __all_sync(0xffffffffu, wait(&bar.s_full[m], s_phase, DEV_TIMEOUT_EPILOGUE)))) break;
         s_phase ^= 1;
         tc_fence_after();
-        const int lim = pos - (rank + it * splits) * kKeys;  // tokens 0 .. lim of the tile count
+        const int lim = pos - (first_of(cur) + it * step_of(cur)) * kKeys;  // tokens 0 .. lim of the tile count
         if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
           // the scores behind the row's position leave S here
 #pragma unroll 1
@@ -664,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       }
       float s0, s1;
       unpair(sum, s0, s1);
-      if (splits == 1) {
+      if (!J || !cur.joint) {
         if (!ok) break;
         do more = walk.next(a, un);
         while (more && m * 128 >= un.rows);
@@ -756,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         }
         cluster_sync();  // nobody writes, or leaves, while another reads its shared memory
         if (!fine) break;
-        more = walk.next(a, un);
+        do more = walk.next(a, un);
+        while (more && !(J && un.joint) && m * 128 >= un.rows);
         if (more && m * 128 < un.rows) load_q(un);
       }
       o_phase ^= cur.rows > 128 ? 3u : 1u;
@@ -773,13 +797,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     int it = 0, mine = tiles_of(un), units = 0;
     auto advance = [&]() {  // the CTA's next tile
       while (more && it == mine) {
+        units += un.joint;
         more = walk.next(a, un);
         it = 0;
         mine = more ? tiles_of(un) : 0;
-        ++units;
       }
-      TileRef x{un.i, un.head, -1, un.len, units};
-      if (more) x.t = rank + it++ * splits;
+      TileRef x{un.i, un.head, -1, un.len, units, units + un.joint};
+      if (more) x.t = first_of(un) + it++ * step_of(un);
       return x;
     };
     TileRef cur = advance(), next = advance();
@@ -791,16 +815,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     int ended = 0;  // shared-out units behind this warp
     bool fine = true;
     auto end_units = [&](int count) {
-      for (; splits > 1 && fine && ended < count; ++ended) fine = unit_end();
+      for (; J && fine && ended < count; ++ended) fine = unit_end();
     };
     for (int n = 0; cur.t >= 0; ++n) {
-      end_units(cur.u);  // (their parts lie over the stages)
+      end_units(cur.before);  // (their parts lie over the stages)
       if (!fine) break;
       const int st = n % kStages;
       const uint32_t free_parity = ((n / kStages) & 1) ^ 1;
       const uint32_t ks = sbase + L::k0 + st * L::k_stage, vs = sbase + L::v0 + st * L::v_stage;
       if (!__all_sync(0xffffffffu, wait(&bar.k_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) {
-        units = cur.u + 1;
+        units = cur.with;
         break;
       }
       if constexpr (Q4) {
@@ -815,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       if (lane == 0) mbar_arrive(&bar.k_full[st]);
       if constexpr (Q4) ld.fetch_k(a, next, next_page);
       if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) {
-        units = cur.u + 1;
+        units = cur.with;
         break;
       }
       ld.store_v(vs);
@@ -891,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         q_phase ^= used;
         if (mine > 0) o_phase ^= used;
         if (mine & 1) p_phase ^= used;
-        if (splits > 1) more = unit_end();  // (not ok: nor is it fine)
+        if (J && un.joint) more = unit_end();  // (not ok: nor is it fine)
         if (ok && more) more = walk.next(a, un);
       }
       __syncwarp();
@@ -902,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         if (!wait_phase(&bar.done, 0, kDrainNs)) set_error(a.err, DEV_TIMEOUT_MMA);
       }
     } else {
-      for (bool more = splits > 1; more;) more = unit_end() && walk.next(a, un);
+      for (bool more = J; more && un.joint;) more = unit_end() && walk.next(a, un);
     }
   }
   __syncwarp();
@@ -912,28 +936,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool Q4>
-cudaError_t launch_d(const ChunkArgs& a, cudaStream_t s) {
-  cudaError_t e = allow_smem<attn_paged_chunk_kernel<D, Q4>>(Layout<D>::smem);
+template <int D, bool Q4, bool J>
+cudaError_t launch_j(const ChunkArgs& a, long long works, int splits, cudaStream_t s) {
+  cudaError_t e = allow_smem<attn_paged_chunk_kernel<D, Q4, J>>(Layout<D>::smem);
   if (e != cudaSuccess) return e;
   // the split of the registers counts on the launch having them
   static const int regs = [] {
     cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, attn_paged_chunk_kernel<D, Q4>) == cudaSuccess ? f.numRegs : 0;
+    return cudaFuncGetAttributes(&f, attn_paged_chunk_kernel<D, Q4, J>) == cudaSuccess ? f.numRegs : 0;
   }();
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const int sms = runtime().num_sms;
-  const long long works = unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1) * a.kv.kv_heads;
-  // units that the batch's rows fill; a history is shared out while that leaves SMs idle
-  // and every CTA keeps two tiles of keys
-  const long long full =
-      ((static_cast<long long>(a.batch.rows) * a.group + kRows - 1) / kRows) * a.kv.kv_heads;
-  int splits = 1;
-  while (splits < kMaxCluster && full * splits * 2 <= sms && a.batch.max_len > splits * 2 * 2 * kKeys) splits *= 2;
-  // and, while an SM has few units, a very long one too, into shares of 32 tiles and more: the longest
-  // unit's CTA would work on alone (12 sequences of up to 24000 keys, 16 heads: 538 us in one piece)
-  if (full < 4ll * sms)
-    splits = std::max(splits, std::min(kMaxCluster, a.batch.max_len / (32 * kKeys)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(splits));
   cfg.blockDim = dim3(kThreads);
@@ -949,22 +961,41 @@ cudaError_t launch_d(const ChunkArgs& a, cudaStream_t s) {
   cfg.numAttrs = runtime().pdl ? 2 : 1;
   // one CTA an SM, or as many clusters as are resident at once
   static std::atomic<int> resident[kMaxCluster + 1];
-  int clusters = splits == 1 ? sms : resident[splits].load(std::memory_order_relaxed);
+  int clusters = J ? resident[splits].load(std::memory_order_relaxed) : runtime().num_sms;
   if (clusters == 0) {
-    if ((e = cudaOccupancyMaxActiveClusters(&clusters, attn_paged_chunk_kernel<D, Q4>, &cfg)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, attn_paged_chunk_kernel<D, Q4, J>, &cfg)) != cudaSuccess) return e;
     clusters = std::max(clusters, 1);
     resident[splits].store(clusters, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(works, clusters) * splits));
-  e = cudaLaunchKernelEx(&cfg, attn_paged_chunk_kernel<D, Q4>, a);
+  e = cudaLaunchKernelEx(&cfg, attn_paged_chunk_kernel<D, Q4, J>, a);
   return e != cudaSuccess ? e : launched();
+}
+
+template <int D, bool Q4>
+cudaError_t launch_d(const ChunkArgs& args, cudaStream_t s) {
+  const int sms = runtime().num_sms;
+  const long long works = unit_total(args.batch.rows, args.batch.b, args.group, kRowShift, 1) * args.kv.kv_heads;
+  // Units that the batch's rows fill.  Histories are shared out while that leaves SMs idle and every
+  // CTA keeps two tiles of keys; and, while an SM has few units, very long ones too, into shares
+  // of 32 tiles and more: the longest unit's CTA would work on alone (12 sequences of up to 24000 keys,
+  // 16 heads: 538 us in one piece)
+  const long long full =
+      ((static_cast<long long>(args.batch.rows) * args.group + kRows - 1) / kRows) * args.kv.kv_heads;
+  int splits = 1;
+  while (splits < kMaxCluster && full * splits * 2 <= sms && args.batch.max_len > splits * 2 * 2 * kKeys) splits *= 2;
+  const int shares = std::min(kMaxCluster, args.batch.max_len / (32 * kKeys));
+  ChunkArgs a = args;
+  a.joint_tiles = splits > 1 ? 2 * splits : 48;
+  if (full < 4ll * sms) splits = std::max(splits, shares);
+  return splits > 1 ? launch_j<D, Q4, true>(a, works, splits, s) : launch_j<D, Q4, false>(a, works, 1, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_paged_chunks(const PagedView& kv, const RaggedView& batch, int heads, int d, int kv_bits,
                                      int min_rows, const __half* q, int ldq, __half* out, int ldo, cudaStream_t s) {
-  const ChunkArgs a{kv, batch, heads, heads / kv.kv_heads, min_rows, q, ldq, out, ldo,
+  const ChunkArgs a{kv, batch, heads, heads / kv.kv_heads, min_rows, 0, q, ldq, out, ldo,
                     1.4426950408889634f / sqrtf(static_cast<float>(d)), runtime().wait_limit_ns, runtime().err};
   if (kv_bits == 4) return d == 128 ? launch_d<128, true>(a, s) : launch_d<64, true>(a, s);
   return d == 128 ? launch_d<128, false>(a, s) : launch_d<64, false>(a, s);
