@@ -112,80 +112,92 @@ struct Unit {
   bool joint;  // shared out over the cluster
 };
 
-// The units of CTA (or cluster) `id` of `stride`, in order: one of each `stride` unit
-// numbers, from the front and from the back by turns (long units tend to come first), 32 looked
-// up at a time, one by each lane; those that hold no rows are passed over.  In a launch of clusters
-// first the cluster's, of joint_tiles tiles and more, then the CTA's own, the shorter ones: a
-// bound on lengths far above the batch's costs a search.
+// The units of CTA (or cluster) `id` of `stride`, in order: one of each `stride` units, from the front
+// and from the back by turns (a sequence's later rows, which see more keys, come first).  A warp
+// counts the units of 32 sequences at a time, a lane each, as it comes to them; sequences that have none cost
+// nothing more.  In a launch of clusters first the cluster's units, those of joint_tiles tiles and
+// more, then the CTA's own, the shorter ones.
 template <bool J>
 struct UnitWalk {
-  long long round, total;
-  int id, stride;
+  int id, stride, total;  // total: more units than a batch of sound spans has (any other ends there)
   bool joint;
-  uint32_t found;
-  int i, head, row0, n, len, c0;
+  int k, i0, before;      // units taken; the 32 sequences' first; units of the sequences before them
+  int row0, n, len;       // the lane's sequence
+  int through, shift;     // units of the sequences up to and with it; minus the first one's number
 
   __device__ __forceinline__ void start(const ChunkArgs& a, int splits) {
-    total = unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1) * a.kv.kv_heads;
+    total = static_cast<int>(unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1));
     joint = J;
     id = static_cast<int>(blockIdx.x) / splits;
     stride = static_cast<int>(gridDim.x) / splits;
-    round = 0;
-    found = 0;
+    k = i0 = before = 0;
+    count(a);
   }
-  // Every lane of the warp calls this and gets the same unit; false: no more.
-  __device__ __forceinline__ bool next(const ChunkArgs& a, Unit& out) {
-    while (found == 0) {
-      if (round * stride >= total) {
-        if (!J || !joint) return false;
-        joint = false;
-        id = static_cast<int>(blockIdx.x);
-        stride = static_cast<int>(gridDim.x);
-        round = 0;
-        continue;
-      }
-      const long long k = round + lane_id();
-      const long long w = k * stride + (k & 1 ? stride - 1 - id : id);
-      round += 32;
-      found = __ballot_sync(0xffffffffu, w < total && look(a, static_cast<int>(w)));
-    }
-    const int from = __ffs(found) - 1;
-    found &= found - 1;
-    const int g = a.group;
-    out.i = __shfl_sync(0xffffffffu, i, from);
-    out.head = __shfl_sync(0xffffffffu, head, from);
-    out.row0 = __shfl_sync(0xffffffffu, row0, from);
-    out.len = __shfl_sync(0xffffffffu, len, from);
-    out.c0 = __shfl_sync(0xffffffffu, c0, from);
-    const int tokens = __shfl_sync(0xffffffffu, n, from);
-    out.first = out.len - tokens;
-    out.rows = min(kRows, tokens * g - out.c0);
-    out.tiles = tiles_of(out.first, out.c0, out.rows, g);
-    out.joint = J && joint;
-    return true;
-  }
-  __device__ __forceinline__ bool look(const ChunkArgs& a, int w) {
-    const int g = a.group, u = w / a.kv.kv_heads;
-    head = w - u * a.kv.kv_heads;
-    int lo = 0, hi = a.batch.b;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (unit_base(a.batch, mid, g, kRowShift, 1) <= u) lo = mid; else hi = mid;
-    }
-    i = lo;
-    const Span sp = ragged_span(a.batch, i, a.err);
+  __device__ __forceinline__ void count(const ChunkArgs& a) {
+    const int lane = static_cast<int>(lane_id()), i = i0 + lane;
+    Span sp{0, 0, 0};
+    if (i < a.batch.b) sp = ragged_span(a.batch, i, a.err);
     row0 = sp.row0;
     n = sp.n;
     len = sp.len;
-    const int rows = sp.n * g;  // at most max_new * group, which the entry point bounds
-    const int rel = u - static_cast<int>(unit_base(a.batch, i, g, kRowShift, 1));
-    const int units = (rows + kRows - 1) / kRows;
-    c0 = (units - 1 - rel) * kRows;  // the later rows, which see more keys, first
-    return sp.n > 0 && rows >= a.min_rows && rel >= 0 && rel < units &&
-           (!J || (tiles_of(len - n, c0, min(kRows, rows - c0), g) >= a.joint_tiles) == joint);
+    const int rows = n * a.group;  // at most max_new * group, which the entry point bounds
+    const int units = n > 0 && rows >= a.min_rows ? (rows + kRows - 1) / kRows : 0;
+    int mine = units, skipped = 0;
+    if (J) {
+      // long ones: the last row's token is at or behind `need`
+      const int need = kKeys * (a.joint_tiles - 1) - (len - n);
+      const int longs = units == 0 || need >= n ? 0 : need <= 0 ? units : units - need * a.group / kRows;
+      mine = joint ? longs : units - longs;
+      skipped = joint ? 0 : longs;
+    }
+    through = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, through, o);
+      if (lane >= o) through += x;
+    }
+    shift = skipped - (through - mine);
   }
-  static __device__ __forceinline__ int tiles_of(int first, int c0, int rows, int g) {
-    return (first + (c0 + rows - 1) / g + kKeys) / kKeys;
+  // Every lane of the warp calls this and gets the same unit; false: no more.
+  __device__ __forceinline__ bool next(const ChunkArgs& a, Unit& out) {
+    int w, u;
+    for (;;) {
+      w = k * stride + (k & 1 ? stride - 1 - id : id);
+      u = w / a.kv.kv_heads;
+      while (u < total) {
+        const int here = __shfl_sync(0xffffffffu, through, 31);
+        if (u < before + here) break;
+        if (i0 + 32 >= a.batch.b) {
+          u = total;
+        } else {
+          before += here;
+          i0 += 32;
+          count(a);
+        }
+      }
+      if (u < total) break;
+      if (!J || !joint) return false;
+      joint = false;
+      id = static_cast<int>(blockIdx.x);
+      stride = static_cast<int>(gridDim.x);
+      k = i0 = before = 0;
+      count(a);
+    }
+    ++k;
+    const int from = __ffs(__ballot_sync(0xffffffffu, u - before < through)) - 1;
+    const int g = a.group;
+    out.i = i0 + from;
+    out.head = w - u * a.kv.kv_heads;
+    out.row0 = __shfl_sync(0xffffffffu, row0, from);
+    out.len = __shfl_sync(0xffffffffu, len, from);
+    const int tokens = __shfl_sync(0xffffffffu, n, from);
+    const int behind = u - before + __shfl_sync(0xffffffffu, shift, from);  // units of later rows
+    out.first = out.len - tokens;
+    out.c0 = ((tokens * g + kRows - 1) / kRows - 1 - behind) * kRows;
+    out.rows = min(kRows, tokens * g - out.c0);
+    out.tiles = (out.first + (out.c0 + out.rows - 1) / g + kKeys) / kKeys;
+    out.joint = J && joint;
+    return true;
   }
 };
 
