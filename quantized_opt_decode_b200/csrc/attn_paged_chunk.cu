@@ -317,9 +317,9 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
   return static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
 }
 
-// One key tile of a unit; t < 0: none.  `before`, `with`: shared-out units before its unit, and with it.
+// One key tile of a unit; t < 0: none.  ends: shared-out units before its own, twice, plus one if its own is.
 struct TileRef {
-  int i, head, t, len, before, with;
+  int i, head, t, len, ends;
 };
 
 // What a loading lane holds of one tile: its part of up to two 8-token blocks.
@@ -607,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       float base = -INFINITY;   // exponent base: log2 of the weights' unit, a whole number
       float limit = -INFINITY;  // the raw score that moves it
       uint64_t sum = 0;        // sums of the even and the odd columns' weights
-      for (int it = 0; it < mine; ++it) {
+      int lim = pos - first_of(cur) * kKeys;  // tokens 0 .. lim of the tile count
+      for (int it = 0; it < mine; ++it, lim -= step_of(cur) * kKeys) {
         if (!(ok = __all_sync(0xffffffffu, wait(&bar.s_full[m], s_phase, DEV_TIMEOUT_EPILOGUE)))) break;
         s_phase ^= 1;
         tc_fence_after();
-        const int lim = pos - (first_of(cur) + it * step_of(cur)) * kKeys;  // tokens 0 .. lim of the tile count
         if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
           // the scores behind the row's position leave S here
 #pragma unroll 1
@@ -757,37 +757,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         }
         cluster_sync();
         const bool fine = cluster_fine();
-        // join the cluster's parts: CTA `rank` takes every splits-th group of four columns
-        constexpr int C4 = D / 4;
+        // join the cluster's parts, 4 W dimensions of a row at a time: columns u .. u + 3 of O's W stretches
+        constexpr int items = D / (4 * W), C4 = D / 4;
         // (an aligned base is at the same offset in every CTA of the launch)
         const float4* parts = reinterpret_cast<const float4*>(smem + L::k0);
-        for (int x = rank * (kSoftmaxWarps * 32) + threadIdx.x; fine && x < cur.rows * C4; x += splits * (kSoftmaxWarps * 32)) {
-          const int jr = x / C4, c4 = x % C4;
-          float top = -INFINITY;
 #pragma unroll 1
-          for (int k = 0; k < splits; ++k) top = fmaxf(top, *cluster.map_shared_rank(&s_m[jr], k));
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float den = 0.f;
-#pragma unroll 1
-          for (int k = 0; k < splits; ++k) {
-            const float mk = *cluster.map_shared_rank(&s_m[jr], k);
-            const float4 pk = *cluster.map_shared_rank(parts + jr * C4 + (c4 ^ (jr & 7)), k);
-            const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - top);
-            den += f * *cluster.map_shared_rank(&s_l[jr], k);
-            acc.x += f * pk.x;
-            acc.y += f * pk.y;
-            acc.z += f * pk.z;
-            acc.w += f * pk.w;
+        for (int x = rank * kRows + static_cast<int>(threadIdx.x); fine && x < items * kRows; x += splits * kRows) {
+          const int jr = x % kRows, u4 = x / kRows;
+          if (jr >= cur.rows) break;
+          float f[kMaxCluster], top = -INFINITY, den = 0.f;
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            f[k] = k < splits ? *cluster.map_shared_rank(&s_m[jr], k) : -INFINITY;
+            top = fmaxf(top, f[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            f[k] = f[k] == -INFINITY ? 0.f : exp2_approx(f[k] - top);
+            if (k < splits) den += f[k] * *cluster.map_shared_rank(&s_l[jr], k);
           }
           const float inv = 1.f / den;
-          const int jc = cur.c0 + jr;
-          __half* dst = a.out + static_cast<size_t>(cur.row0 + jc / g) * a.ldo + (cur.head * g + jc % g) * D;
-          const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+          float o[W][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = c4 * 4 + e;
-            dst[W * (col % (D / W)) + col / (D / W)] = __float2half_rn(o[e]);
+          for (int q = 0; q < W; ++q) {
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {
+              if (k >= splits) continue;
+              const float4 pk = *cluster.map_shared_rank(parts + jr * C4 + ((q * items + u4) ^ (jr & 7)), k);
+              acc.x += f[k] * pk.x;
+              acc.y += f[k] * pk.y;
+              acc.z += f[k] * pk.z;
+              acc.w += f[k] * pk.w;
+            }
+            o[q][0] = acc.x * inv;
+            o[q][1] = acc.y * inv;
+            o[q][2] = acc.z * inv;
+            o[q][3] = acc.w * inv;
           }
+          const int jc = cur.c0 + jr;
+          __half* dst = a.out + static_cast<size_t>(cur.row0 + jc / g) * a.ldo + (cur.head * g + jc % g) * D + u4 * (4 * W);
+#pragma unroll
+          for (int e = 0; e < 4 * W; e += 8)  // dimension e of these: stretch e % W, column e / W
+            *reinterpret_cast<uint4*>(dst + e) =
+                make_uint4(pack_half2(o[e % W][e / W], o[(e + 1) % W][(e + 1) / W]),
+                           pack_half2(o[(e + 2) % W][(e + 2) / W], o[(e + 3) % W][(e + 3) / W]),
+                           pack_half2(o[(e + 4) % W][(e + 4) / W], o[(e + 5) % W][(e + 5) / W]),
+                           pack_half2(o[(e + 6) % W][(e + 6) / W], o[(e + 7) % W][(e + 7) / W]));
         }
         cluster_sync();  // nobody writes, or leaves, while another reads its shared memory
         if (!fine) break;
@@ -814,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         it = 0;
         mine = more ? tiles_of(un) : 0;
       }
-      TileRef x{un.i, un.head, -1, un.len, units, units + un.joint};
+      TileRef x{un.i, un.head, -1, un.len, 2 * units + un.joint};
       if (more) x.t = first_of(un) + it++ * step_of(un);
       return x;
     };
@@ -830,13 +846,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       for (; J && fine && ended < count; ++ended) fine = unit_end();
     };
     for (int n = 0; cur.t >= 0; ++n) {
-      end_units(cur.before);  // (their parts lie over the stages)
+      end_units(cur.ends >> 1);  // (their parts lie over the stages)
       if (!fine) break;
       const int st = n % kStages;
       const uint32_t free_parity = ((n / kStages) & 1) ^ 1;
       const uint32_t ks = sbase + L::k0 + st * L::k_stage, vs = sbase + L::v0 + st * L::v_stage;
       if (!__all_sync(0xffffffffu, wait(&bar.k_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) {
-        units = cur.with;
+        units = (cur.ends + 1) >> 1;
         break;
       }
       if constexpr (Q4) {
@@ -851,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       if (lane == 0) mbar_arrive(&bar.k_full[st]);
       if constexpr (Q4) ld.fetch_k(a, next, next_page);
       if (!__all_sync(0xffffffffu, wait(&bar.v_empty[st], free_parity, DEV_TIMEOUT_PRODUCER))) {
-        units = cur.with;
+        units = (cur.ends + 1) >> 1;
         break;
       }
       ld.store_v(vs);
@@ -996,10 +1012,9 @@ cudaError_t launch_d(const ChunkArgs& args, cudaStream_t s) {
       ((static_cast<long long>(args.batch.rows) * args.group + kRows - 1) / kRows) * args.kv.kv_heads;
   int splits = 1;
   while (splits < kMaxCluster && full * splits * 2 <= sms && args.batch.max_len > splits * 2 * 2 * kKeys) splits *= 2;
-  const int shares = std::min(kMaxCluster, args.batch.max_len / (32 * kKeys));
   ChunkArgs a = args;
   a.joint_tiles = splits > 1 ? 2 * splits : 48;
-  if (full < 4ll * sms) splits = std::max(splits, shares);
+  while (splits < kMaxCluster && full < 4ll * sms && args.batch.max_len / (2 * splits) >= 32 * kKeys) splits *= 2;
   return splits > 1 ? launch_j<D, Q4, true>(a, works, splits, s) : launch_j<D, Q4, false>(a, works, 1, s);
 }
 
