@@ -26,17 +26,20 @@
 //                    one is in its softmax, the other's run.
 // One CTA an SM walks the units (256 query rows of a sequence and key/value head) that fall to it:
 // every role runs on into the next unit on its own, so the stores of one unit overlap the
-// products of the next; unit numbers that hold no rows (paged_math.h) cost a lane of a search,
-// not a CTA.  A long history of few units is shared out over a cluster of CTAs, whose
-// (maximum, sum, O) are joined over distributed shared memory in a fixed order.
+// products of the next.  Where the bounds allow few units, or long ones, the launch is one of clusters: each
+// shares out the units of many tiles that fall to it, whose (maximum, sum, O) are joined over
+// distributed shared memory in a fixed order; then its CTAs walk the shorter ones alone.  The bounds may be
+// far above the batch (a captured graph), so clusters are as many as are resident at once and not one a
+// possible unit (32 sequences, four of them chunks, 56 heads, under a bound of 32768 keys: 174 us against 148
+// under their own; 776 with a cluster a unit).
 // Every wait is bounded; on expiry the error word is set and the CTA unwinds.
 //
 // Measured (B200; two sequences of 1900 to 2048 new tokens over 5600 to 6100 keys, 32 heads, d = 128,
-// 4 bit): 417 us = 775 TFLOP/s, 0.47 of the library product's rate.  A pair of row tiles takes some
-// 4600 cycles a key tile against 2100 of products: scores, softmax, P and products are one chain
+// 4 bit): 396 to 409 us = 790 to 817 TFLOP/s, 0.48 to 0.50 of the library product's rate.  A pair of row tiles
+// takes some 4500 cycles a key tile against 2100 of products: scores, softmax, P and products are one chain
 // per row tile, of which the 16-lane exponential unit (2048 cycles a pair) and the issue slots
 // (9500 instructions, 3700 of them the dequantizer's) make up the most.  Tried, at the
-// same sizes: scores of 64 keys, twice, so that the next are there when a softmax ends (464 us: twice
+// same sizes (the last three where the kept form took 417): scores of 64 keys, twice, so that the next are there when a softmax ends (464 us: twice
 // the hand-offs); one thread a row tile issuing the products (547 us against 451: both softmaxes
 // then run at the same time); a quarter of the exponentials as polynomials (446 us: issue slots);
 // loops rolled up for the instruction cache (519 us); four loading warps (446 us); the largest score of the
