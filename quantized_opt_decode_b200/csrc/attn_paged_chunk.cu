@@ -30,13 +30,13 @@
 // shares out the units of many tiles that fall to it, whose (maximum, sum, O) are joined over
 // distributed shared memory in a fixed order; then its CTAs walk the shorter ones alone.  The bounds may be
 // far above the batch (a captured graph), so clusters are as many as are resident at once and not one a
-// possible unit (32 sequences, four of them chunks, 56 heads, under a bound of 32768 keys: 174 us against 148
+// possible unit (32 sequences, four of them chunks, 56 heads, under a bound of 32768 keys: 173 us against 146
 // under their own; 776 with a cluster a unit).
 // Every wait is bounded; on expiry the error word is set and the CTA unwinds.
 //
 // Measured (B200; two sequences of 1900 to 2048 new tokens over 5600 to 6100 keys, 32 heads, d = 128,
-// 4 bit): 396 to 409 us = 790 to 817 TFLOP/s, 0.48 to 0.50 of the library product's rate.  A pair of row tiles
-// takes some 4500 cycles a key tile against 2100 of products: scores, softmax, P and products are one chain
+// 4 bit): 392 to 400 us = 808 to 824 TFLOP/s, 0.49 to 0.50 of the library product's rate.  A pair of row tiles
+// takes some 4400 cycles a key tile against 2100 of products: scores, softmax, P and products are one chain
 // per row tile, of which the 16-lane exponential unit (2048 cycles a pair) and the issue slots
 // (9500 instructions, 3700 of them the dequantizer's) make up the most.  Tried, at the
 // same sizes (the last three where the kept form took 417): scores of 64 keys, twice, so that the next are there when a softmax ends (464 us: twice
@@ -67,8 +67,8 @@ constexpr int kStages = 2;
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kThreads = (kMmaWarp + 4) * 32;  // whole warpgroups, which share a register count
-// Registers a thread by role, out of the launch's 640 * 96.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kLoadRegs = 72, kMmaRegs = 64;
+// Registers a thread by role, out of the launch's 640 * 96 (136, 72 and 64: 405 us where this takes 395).
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kLoadRegs = 80, kMmaRegs = 64;
 static_assert(256 * kSoftmaxRegs + 256 * kLoadRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs,
               "a split above the launch's registers would wait for ever");
 constexpr int kMaxCluster = 8;
