@@ -15,7 +15,7 @@
 
 #include "common.cuh"
 #include "flexq.h"
-#include "kernels.h"
+#include "kernels_serving.h"
 
 namespace flexq {
 

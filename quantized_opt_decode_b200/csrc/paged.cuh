@@ -3,7 +3,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "kernels.h"
+#include "kernels_serving.h"
 #include "paged_math.h"
 
 namespace flexq {

@@ -7,7 +7,7 @@
 #include <atomic>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "kernels_serving.h"
 
 namespace flexq {
 
