@@ -647,6 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
           }
           top = fmaxf(top, top1);
           if (__any_sync(0xffffffffu, top > limit)) {  // (from -inf: any finite score)
+            // P of the columns before, and O after an earlier move in this tile, were stored by this
+            // thread and are read back here: only the wait orders the two
+            tmem_st_wait();
             const float nb = top > limit ? ceilf(top * a.scale_log2) : base;
             const float alpha = base == -INFINITY ? 0.f : exp2_approx(base - nb);
             base = nb;

@@ -1,0 +1,65 @@
+"""Paged attention where its running softmax and its sums can go wrong: scores that outgrow
+the exponent base inside a key tile, weights far below the largest, and long histories of
+values of one sign, against 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import paged_helpers as ph  # noqa: E402
+from gpu_helpers import fq, to_dev, to_host  # noqa: E402
+from test_gpu_paged import Dev, check_attention  # noqa: E402
+
+
+def set_levels(pg, i, level, boost):
+    """Key p of sequence i becomes the constant vector level[p] (exact in both caches); its value
+    is multiplied by 2^boost[p] (exact too)."""
+    for p in range(pg.lens[i]):
+        at, sl = pg.where(i, p)
+        if pg.bits == 16:
+            pg.k[at, :, sl] = level[p]
+            pg.v[at, :, sl] = np.ldexp(pg.v[at, :, sl], int(boost[p]))
+        else:
+            pg.k[at, :, sl] = 0
+            pg.km[at, :, sl, :, 0], pg.km[at, :, sl, :, 1] = level[p], 0
+            pg.vm[at, :, sl] = np.ldexp(pg.vm[at, :, sl], int(boost[p]))
+
+
+# base-2 logarithms of the weights of 32-key pieces: they outgrow 2^8 at each piece of a tile,
+# in the first tile and later ones, twice and three times in one, by more than fp16 can scale by
+STEPS = [
+    (0, 9, 9, 9, 9, 9, 9, 9),
+    (0, 0, 9, 9, 9, 9, 9, 9),
+    (0, 0, 0, 9, 9, 9, 9, 9),
+    (0, 0, 0, 0, 9, 9, 9, 9),
+    (0, 0, 0, 0, 0, 9, 18, 18),
+    (0, 9, 18, 27, 27, 27, 27, 27),
+    (0, 0, 0, 0, 0, 9, 18, 27),
+    (0, 0, 0, 0, 26, 26, 26, 52),
+    (0, 26, 26, 26, 26, 52, 52, 52),
+    (40, 0, 49, 0, 10, 58, 0, 67),
+]
+
+
+@pytest.mark.parametrize("steps", STEPS)
+@pytest.mark.parametrize("bits,d", [(4, 128), (4, 64), (16, 128), (16, 64)])
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_scores_that_outgrow_the_base_inside_a_tile(steps, bits, d, new):
+    """Every piece's values are so much larger than the later ones' that each counts in the
+    result: a piece whose weights are not scaled with the base shows."""
+    past = 32 * len(steps)
+    pg = ph.Paged(bits, 4, 2, d, 16, (new,), (past,), seed=len(steps) + sum(steps))
+    log2 = np.concatenate([np.repeat(steps, 32), np.full(new, steps[-1])]).astype(float)
+    boost = np.clip(max(steps) - log2, 0, 13)
+    # scores q k / sqrt d of q = 1: a step of `log2` in base 2
+    level = (log2 / np.log2(np.e) / np.sqrt(d)).astype(np.float16)
+    set_levels(pg, 0, level, boost)
+    q = np.ones((pg.rows, 4 * d), np.float16)
+    # some rows see half or none of the growth, or its reverse: their bases move elsewhere or not at all
+    q *= np.array([1, 0.5, 1, 0, 1, -0.25], np.float16)[np.arange(pg.rows) % 6][:, None]
+    dv = Dev(pg)
+    out = torch.full((pg.rows, 4 * d), float("nan"), dtype=torch.float16, device="cuda")
+    fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), 4 * d, out, 4 * d)
+    fq.flexq_device_status()
+    check_attention(pg, q, to_host(out))
