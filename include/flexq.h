@@ -358,7 +358,8 @@ typedef struct {
 size_t flexq_paged_kv_bytes(const flexq_config* cfg, int kv_heads, int num_pages, int page_size);
 
 /* Appends the new tokens' keys and values: k_dev, v_dev fp16 [rows][ld] (head j
- * at columns j*d ..), stored as flexq_kv_append stores them (the same codes).
+ * at columns j*d ..), stored as flexq_kv_append stores them (the same codes; a NaN or an
+ * infinity touches no code or pair outside its own 64-element group of its own token).
  * rope (NULL: none, as in OPT): the keys are rotated by their positions
  * first, and with q_dev the queries (fp16 [rows][ldq], cfg->heads heads) are
  * rotated into q_out_dev [rows][ldqo] (q_out may be q with the same stride); q_dev must be

@@ -23,6 +23,8 @@
 // The codes are exactly those of flexq_quantize on the (rotated) fp16 rows:
 // rotation multiplies and adds in fp32 without contraction and rounds once to
 // fp16, then the shared group rule applies.
+#include <math.h>
+
 #include "paged.cuh"
 #include "quant_common.cuh"
 
@@ -133,11 +135,11 @@ __device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y) {
 // x / 15 correctly rounded: the product with the rounded reciprocal is within an
 // ulp, its remainder is exact in one multiply-add, and one more with the reciprocal
 // rounds to the quotient (Markstein, 1990).  x: a difference of fp16 values, so
-// nothing underflows.
+// nothing underflows; the remainder of an infinity is NaN and is left out.
 __device__ __forceinline__ float fifteenth(float x) {
   constexpr float y = 1.0f / 15.0f;
   const float q = __fmul_rn(x, y);
-  return fmaf(fmaf(-15.0f, q, x), y, q);
+  return fabsf(x) == INFINITY ? x : fmaf(fmaf(-15.0f, q, x), y, q);
 }
 
 struct Group {
@@ -164,7 +166,8 @@ __device__ __forceinline__ Group group_of(uint32_t range) {
 // has 25 bits and s has 11, so a / s, unless it is one, is at least 2^-11 of half an ulp away from every
 // midpoint; and it never is one, since the product of an odd 25-bit number with s does not fit a's
 // 24 bits.  x >= min, so codes are never negative; only a subnormal scale can have been rounded down
-// so far that a quotient exceeds 15.5.
+// so far that a quotient exceeds 15.5.  NaN (of a value, or of a group with an infinity: 0 * inf) takes
+// code 0, as in the codec; left as it is, its bits would carry into the word's other codes.
 constexpr uint32_t kCodeBias = 0x4B400000u;
 __device__ __forceinline__ void chunk_codes(const uint4& raw, const Group& g, uint32_t (&c)[8]) {
   float x[8];
@@ -173,7 +176,7 @@ __device__ __forceinline__ void chunk_codes(const uint4& raw, const Group& g, ui
   for (int e = 0; e < 8; ++e) {
     const float d = __fsub_rn(x[e], g.mn);
     const float q = __fmul_rn(d, g.inv);
-    c[e] = __float_as_uint(__fadd_rn(fmaf(fmaf(-g.sc, q, d), g.inv, q), 12582912.0f));
+    c[e] = __float_as_uint(__fadd_rn(fmaxf(fmaf(fmaf(-g.sc, q, d), g.inv, q), 0.0f), 12582912.0f));
   }
   if (g.sc < 0x1p-14f) {
 #pragma unroll
@@ -205,7 +208,7 @@ __device__ __forceinline__ void quantize(const uint4& ra, const uint4& rb, const
     chunk_codes(ra, g, ca);
     chunk_codes(rb, g, cb);
   } else {
-    constexpr uint32_t kNone = 0x7c007c00u;  // (inf, inf)
+    constexpr uint32_t kNone = 0x7fff7fffu;  // NaN twice, which the minimum passes over
     uint32_t r0 = min2(s.ea < 64 ? a : kNone, s.eb < 64 ? b : kNone);
     uint32_t r1 = min2(s.ea < 64 ? kNone : a, s.eb < 64 ? kNone : b);
 #pragma unroll
