@@ -660,15 +660,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
               unpair(sums[k], s0, s1);
               sums[k] = pair(__float_as_uint(s0 * alpha), __float_as_uint(s1 * alpha));
             }
-            const __half2 alpha2 = __float2half2_rn(alpha);
 #pragma unroll 1
             for (int q = 0; q < ch; ++q) {
               uint32_t o[16];
               tmem_read_x16(s_col + 16 * q, o);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const __half2 y = __hmul2(as_half2(o[e]), alpha2);
-                o[e] = *reinterpret_cast<const uint32_t*>(&y);
+                // (in fp32: the factor itself may lie below fp16's range)
+                const float2 y = __half22float2(as_half2(o[e]));
+                o[e] = pack_half2(y.x * alpha, y.y * alpha);
               }
               tmem_st_x16(s_col + 16 * q, o);
             }

@@ -63,3 +63,27 @@ def test_scores_that_outgrow_the_base_inside_a_tile(steps, bits, d, new):
     fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), 4 * d, out, 4 * d)
     fq.flexq_device_status()
     check_attention(pg, q, to_host(out))
+
+
+@pytest.mark.parametrize("bits,d", [(4, 128), (4, 64), (16, 128), (16, 64)])
+@pytest.mark.parametrize("jump", [22, 24.5, 26, 30])
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_weights_above_their_base_outlive_a_move_of_it(bits, d, jump, new):
+    """The second and third piece of a tile reach 2^7.5 of the first one's base without moving
+    it; the fourth moves it by 2^22 to 2^30.  Their weights are then 2^-14.5 to 2^-22.5 of the largest,
+    and their values, of one sign, make up for it."""
+    steps = [-20, -20, -20, -20, 0, 7.5, 7.5, jump]
+    pg = ph.Paged(bits, 4, 2, d, 16, (new,), (256,), seed=int(2 * jump) + new)
+    if bits == 16:
+        pg.v = np.abs(pg.v)
+    else:
+        pg.vm[..., 0] = np.where(np.isnan(pg.vm[..., 0]), np.nan, 0)  # values: code * scale
+    log2 = np.concatenate([np.repeat(steps, 32), np.full(new, jump)])
+    boost = np.repeat([0, 0, 0, 0, 0, 12, 12, 0], 32).tolist() + [0] * new
+    set_levels(pg, 0, (log2 / np.log2(np.e) / np.sqrt(d)).astype(np.float16), boost)
+    q = np.ones((pg.rows, 4 * d), np.float16)
+    dv = Dev(pg)
+    out = torch.full((pg.rows, 4 * d), float("nan"), dtype=torch.float16, device="cuda")
+    fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), 4 * d, out, 4 * d)
+    fq.flexq_device_status()
+    check_attention(pg, q, to_host(out))
