@@ -50,7 +50,7 @@ struct PagedAttnArgs {
   __half* out;
   int ldo;
   float scale_log2;
-  float slack;        // 8 / scale_log2
+  float slack;        // kWeightSlack / scale_log2
   uint32_t by_group;  // c / group = (c * by_group) >> 16 for the columns c < 16
   uint32_t* err;
 };
@@ -203,7 +203,7 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
   }
 
   float o[MT][NT][4];
-  float mx[NT][2], off[NT][2], sum[NT][2];  // base of the exponents (raw score), -base * scale, sum of weights
+  float mx[NT][2], off[NT][2], sum[NT][2];  // base of the exponents (raw score), bias - base * scale, sum of weights
   int last[NT][2];  // position of the lane's two rows of each column tile
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -309,9 +309,8 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
             if (p > last[nt][e & 1]) s[km][nt][e] = -INFINITY;
         }
     }
-    // The exponent base of a row only moves when a score outgrows it by 2^8, so that O is
-    // rarely rescaled; the weights stay below 2^8 in fp16 (a relative rounding, 2^-11,
-    // wherever the base is; the sum keeps fp32).
+    // The exponent base of a row only moves when a score outgrows it by 2^7, so that O is
+    // rarely rescaled (kWeightBias: what the weights are in fp16).
     uint32_t pt[NT][2 * KM];
     float tm[NT][2];
     bool grew = false;
@@ -337,7 +336,7 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
           m = m > mx[nt][e] + a.slack ? m : mx[nt][e];
           alpha[e] = m == -INFINITY ? 1.f : exp2_approx((mx[nt][e] - m) * a.scale_log2);
           mx[nt][e] = m;
-          off[nt][e] = m == -INFINITY ? 0.f : -m * a.scale_log2;  // no key of the row so far: 0
+          off[nt][e] = m == -INFINITY ? 0.f : fmaf(-m, a.scale_log2, kWeightBias);  // no key of the row so far: 0
           sum[nt][e] *= alpha[e];
         }
 #pragma unroll
@@ -577,7 +576,7 @@ cudaError_t launch_attn_paged(const PagedView& kv, const RaggedView& batch, int 
   const int group = heads / kv.kv_heads;
   // ceil(2^16 / group): exact quotients for c < 16, group <= 16 (the error c * group / 2^16 stays below 1 / group)
   const PagedAttnArgs a{kv,  batch, heads,      group,           q,
-                        ldq, out,   ldo,        scale_log2,      8.f / scale_log2,
+                        ldq, out,   ldo,        scale_log2,      kWeightSlack / scale_log2,
                         static_cast<uint32_t>((65536 + group - 1) / group), runtime().err};
   if (kv_bits == 4) return d == 128 ? launch_d<128, true>(a, s) : launch_d<64, true>(a, s);
   return d == 128 ? launch_d<128, false>(a, s) : launch_d<64, false>(a, s);

@@ -9,10 +9,9 @@
 // so 2 x 4 * 128 * 128 * d flops stand against one pass over the tile's codes.  Roles:
 //   warps 0-3, 4-7   softmax of row tile 0, 1: a thread owns a row (a TMEM lane), so the
 //                    running maximum and sum need no exchange.  The exponent base is a whole
-//                    power of two that only moves when a score outgrows it by 2^8: P then
-//                    stays below 2^8 in fp16 (a relative rounding, so the base does not
-//                    matter), a tile's scores are read once, 32 columns at a time, and where the
-//                    base moves, the factor for O and for the P already stored is exact;
+//                    power of two that only moves when a score outgrows it by 2^7; a tile's scores
+//                    are read once, 32 columns at a time, and where the base moves, the factor
+//                    for O and for the P already stored is exact (kWeightBias: what P is in fp16);
 //   warps 8-15       bring K and V: pages looked up two tiles ahead, codes fetched one
 //                    tile ahead into registers, dequantized (rounded once to fp16, as the codec's
 //                    values) and stored in the 128-byte-swizzled layout; a
@@ -653,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
             const float nb = top > limit ? ceilf(top * a.scale_log2) : base;
             const float alpha = base == -INFINITY ? 0.f : exp2_approx(base - nb);
             base = nb;
-            limit = (nb + 8.f) * inv_scale;
+            limit = (nb + kWeightSlack) * inv_scale;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float s0, s1;
@@ -683,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
               }
             }
           }
-          const uint32_t off = __float_as_uint(base == -INFINITY ? 0.f : -base);
+          const uint32_t off = __float_as_uint(base == -INFINITY ? 0.f : kWeightBias - base);
           const uint64_t off2 = pair(off, off), scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
           uint32_t p[16];
 #pragma unroll

@@ -8,6 +8,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 import paged_helpers as ph  # noqa: E402
+from paged_bounds import attention_rows  # noqa: E402
 from gpu_helpers import fq, to_dev, to_host  # noqa: E402
 from test_gpu_paged import Dev, check_attention  # noqa: E402
 
@@ -15,15 +16,16 @@ from test_gpu_paged import Dev, check_attention  # noqa: E402
 def set_levels(pg, i, level, boost):
     """Key p of sequence i becomes the constant vector level[p] (exact in both caches); its value
     is multiplied by 2^boost[p] (exact too)."""
-    for p in range(pg.lens[i]):
-        at, sl = pg.where(i, p)
-        if pg.bits == 16:
-            pg.k[at, :, sl] = level[p]
-            pg.v[at, :, sl] = np.ldexp(pg.v[at, :, sl], int(boost[p]))
-        else:
-            pg.k[at, :, sl] = 0
-            pg.km[at, :, sl, :, 0], pg.km[at, :, sl, :, 1] = level[p], 0
-            pg.vm[at, :, sl] = np.ldexp(pg.vm[at, :, sl], int(boost[p]))
+    p = np.arange(pg.lens[i])
+    at, sl = pg.table[i, p // pg.page], p % pg.page
+    level, boost = np.asarray(level), np.asarray(boost, int)
+    if pg.bits == 16:
+        pg.k[at, :, sl] = level[:, None, None]
+        pg.v[at, :, sl] = np.ldexp(pg.v[at, :, sl], boost[:, None, None])
+    else:
+        pg.k[at, :, sl] = 0
+        pg.km[at, :, sl, :, 0], pg.km[at, :, sl, :, 1] = level[:, None, None], 0
+        pg.vm[at, :, sl] = np.ldexp(pg.vm[at, :, sl], boost[:, None, None, None])
 
 
 # base-2 logarithms of the weights of 32-key pieces: they outgrow 2^8 at each piece of a tile,
@@ -87,3 +89,33 @@ def test_weights_above_their_base_outlive_a_move_of_it(bits, d, jump, new):
     fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), 4 * d, out, 4 * d)
     fq.flexq_device_status()
     check_attention(pg, q, to_host(out))
+
+
+@pytest.mark.parametrize("bits,new", [(4, 1), (4, 20), (16, 1), (16, 20)])
+@pytest.mark.parametrize("n,sink", [(32, 0), (33, 3), (128, 100), (131072, 70000)])
+def test_a_flat_history_behind_one_large_weight(bits, new, n, sink):
+    """Equal weights, 2^20 to 2^28 below that of one key whose value is zero: the result is what
+    they sum up to, however many there are."""
+    d = 128
+    pg = ph.Paged(bits, 1, 1, d, 1024, (new,), (n - new,), seed=new, spare=1)
+    if bits == 16:
+        pg.v = np.abs(pg.v)
+    else:
+        pg.vm[..., 0] = np.where(np.isnan(pg.vm[..., 0]), np.nan, 0)  # values: code * scale
+    at, sl = pg.where(0, sink)
+    (pg.v if bits == 16 else pg.vm)[at, :, sl] = 0
+    boost = 12 if n < 1000 else 0  # (else the result is below fp16)
+    q = np.ones((new, d), np.float16)
+    for below in (20, 25.25, 28):
+        log2 = np.zeros(n)
+        log2[sink] = below
+        set_levels(pg, 0, (log2 / np.log2(np.e) / np.sqrt(d)).astype(np.float16), np.full(n, boost))
+        boost = 0  # (the values keep it)
+        dv = Dev(pg)
+        out = torch.full((new, d), float("nan"), dtype=torch.float16, device="cuda")
+        fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), d, out, d)
+        fq.flexq_device_status()
+        k, v = pg.history(0)
+        ref, tol = attention_rows(q, k[:, 0], v[:, 0], n - new)
+        over = np.abs(to_host(out).astype(np.float64) - ref) / tol
+        assert over.max() <= 1, (below, over.max())
