@@ -133,7 +133,15 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
-template <int D, bool Q4, int NT>
+// The tensor core truncates, always towards zero, when it adds to its accumulator: O lost 3e-5 of
+// its size over 128 tiles a warp, and 8e-4 over 4096 (262144 keys of values of one sign).  Fold: a
+// tile's products start from zero and are added to O with rounding, which over n tiles is at most
+// n 2^-25 off and has no direction of its own (4e-5 over 4096).  It costs 4 % (4736 histories of 262144
+// keys, one head: 37.9 ms with it, 36.5 without), so shares of up to kPlainTiles tiles, whose 512 additions of at most 2^-23
+// each cannot come to more than a quarter of the output's own rounding, 2^-13, are added up in the accumulator.
+constexpr int kPlainTiles = 256;
+
+template <int D, bool Q4, int NT, bool Fold>
 __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const PagedAttnArgs a) {
   using T = Tile<D, Q4>;
   constexpr int NC = 8 * NT;       // columns: query rows
@@ -351,10 +359,17 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
       for (int km = 0; km < KM; ++km) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[km][nt][e] = exp2_approx(fmaf(s[km][nt][e], a.scale_log2, off[nt][e & 1]));
-        sum[nt][0] += s[km][nt][0] + s[km][nt][2];
-        sum[nt][1] += s[km][nt][1] + s[km][nt][3];
         pt[nt][2 * km] = movmatrix_trans(pack_half2(s[km][nt][0], s[km][nt][1]));
         pt[nt][2 * km + 1] = movmatrix_trans(pack_half2(s[km][nt][2], s[km][nt][3]));
+      }
+
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = s[0][nt][e] + s[0][nt][e + 2];
+        if (KM == 2) l += s[KM - 1][nt][e] + s[KM - 1][nt][e + 2];
+        sum[nt][e] += l;
       }
 
     // O^T += V^T P^T
@@ -397,8 +412,17 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
             dequant_word(word_of(w, 2 * h + 1), sc[0], mn[0], sc[1], mn[1], sc[2], mn[2], sc[3], mn[3], hi);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_16816(o[2 * q + h][nt], lo[0], hi[0], lo[1], hi[1], pt[nt][0], pt[nt][1]);
-              mma_16816(o[2 * q + h][nt], lo[2], hi[2], lo[3], hi[3], pt[nt][2 * KM - 2], pt[nt][2 * KM - 1]);
+              float(&to)[4] = o[2 * q + h][nt];
+              if (Fold) {
+                float part[4];
+                mma_16816_first(part, lo[0], hi[0], lo[1], hi[1], pt[nt][0], pt[nt][1]);
+                mma_16816(part, lo[2], hi[2], lo[3], hi[3], pt[nt][2 * KM - 2], pt[nt][2 * KM - 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) to[e] += part[e];
+              } else {
+                mma_16816(to, lo[0], hi[0], lo[1], hi[1], pt[nt][0], pt[nt][1]);
+                mma_16816(to, lo[2], hi[2], lo[3], hi[3], pt[nt][2 * KM - 2], pt[nt][2 * KM - 1]);
+              }
             }
           }
         }
@@ -412,7 +436,16 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
         const int u = 2 * mt + ((lane >> 3) & 1);
         ldmatrix4_trans(smem_u32(st + T::side + y * T::row + ((u ^ (y & 7)) * 16)), f);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(o[mt][nt], f[0], f[1], f[2], f[3], pt[nt][0], pt[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if (Fold) {
+            float part[4];
+            mma_16816_first(part, f[0], f[1], f[2], f[3], pt[nt][0], pt[nt][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][nt][e] += part[e];
+          } else {
+            mma_16816(o[mt][nt], f[0], f[1], f[2], f[3], pt[nt][0], pt[nt][1]);
+          }
+        }
       }
     }
   }
@@ -507,8 +540,9 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
 struct Plan {
   int warps, splits;
 };
-Plan plan_rows(long long units, int max_len, int tile, int sms) {
-  const long long tiles = (max_len + tile - 1) / tile;
+long long tiles_of(int max_len, int tile) { return (static_cast<long long>(max_len) + tile - 1) / tile; }
+Plan plan_balanced(long long units, int max_len, int tile, int sms) {
+  const long long tiles = tiles_of(max_len, tile);
   if (tiles <= 2) return {static_cast<int>(tiles), 1};  // no warp without a tile
   if (units >= 32ll * sms) return {2, 1};
   Plan best{4, 1};
@@ -527,14 +561,22 @@ Plan plan_rows(long long units, int max_len, int tile, int sms) {
   const long long splits = std::min({static_cast<long long>(kMaxCluster), rounds, static_cast<long long>(max_len / 512)});
   return splits > 1 && units * splits >= 5ll * sms ? Plan{4, static_cast<int>(splits)} : best;
 }
+// The same, but no warp's share of a history longer than 4096 tiles (as far as 64 warps a history
+// go): a sum of more roundings could, all in one direction, reach 2^-12.
+Plan plan_rows(long long units, int max_len, int tile, int sms) {
+  Plan p = plan_balanced(units, max_len, tile, sms);
+  const long long tiles = tiles_of(max_len, tile);
+  while (p.warps < kMaxWarps && tiles > 4096ll * p.warps * p.splits) p.warps *= 2;
+  while (p.splits < kMaxCluster && tiles > 4096ll * p.warps * p.splits) p.splits = std::min(2 * p.splits, kMaxCluster);
+  return p;
+}
 
-template <int D, bool Q4, int NT>
-cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
+template <int D, bool Q4, int NT, bool Fold>
+cudaError_t launch_plan(const PagedAttnArgs& a, const Plan& plan, cudaStream_t s) {
   using T = Tile<D, Q4>;
   static_assert(T::stages * T::bytes >= 8 * NT * D * 4, "a warp's ring holds its partial output");
-  cudaError_t e = allow_smem<attn_paged_rows_kernel<D, Q4, NT>>(kMaxWarps * T::stages * T::bytes);
+  cudaError_t e = allow_smem<attn_paged_rows_kernel<D, Q4, NT, Fold>>(kMaxWarps * T::stages * T::bytes);
   if (e != cudaSuccess) return e;
-  const Plan plan = plan_rows(static_cast<long long>(a.batch.b) * a.kv.kv_heads, a.batch.max_len, T::keys, runtime().num_sms);
   const int warps = plan.warps, splits = plan.splits;
   const long long units = static_cast<long long>(a.batch.b) * a.kv.kv_heads;
   const int smem = warps * T::stages * T::bytes;
@@ -551,8 +593,16 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = runtime().pdl ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<D, Q4, NT>, a);
+  e = cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<D, Q4, NT, Fold>, a);
   return e != cudaSuccess ? e : launched();
+}
+
+template <int D, bool Q4, int NT>
+cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
+  const long long units = static_cast<long long>(a.batch.b) * a.kv.kv_heads;
+  const Plan plan = plan_rows(units, a.batch.max_len, Tile<D, Q4>::keys, runtime().num_sms);
+  const bool plain = tiles_of(a.batch.max_len, Tile<D, Q4>::keys) <= static_cast<long long>(kPlainTiles) * plan.warps * plan.splits;
+  return plain ? launch_plan<D, Q4, NT, false>(a, plan, s) : launch_plan<D, Q4, NT, true>(a, plan, s);
 }
 
 template <int D, bool Q4>

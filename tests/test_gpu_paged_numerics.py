@@ -119,3 +119,65 @@ def test_a_flat_history_behind_one_large_weight(bits, new, n, sink):
         ref, tol = attention_rows(q, k[:, 0], v[:, 0], n - new)
         over = np.abs(to_host(out).astype(np.float64) - ref) / tol
         assert over.max() <= 1, (below, over.max())
+
+
+def _positive_pool(bits, n, d, page=1024):
+    """A pool whose pages 0, 1, .. hold n keys in (-1/2, 1/2) and values in (1/2, 3/2), on the device."""
+    pages = -(-n // page)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n + bits)
+    if bits == 16:
+        k = (torch.rand(pages, 1, page, d, device="cuda", generator=gen) - 0.5).half()
+        v = (torch.rand(pages, 1, page, d, device="cuda", generator=gen) + 0.5).half()
+        return (k, v, None, None), k.view(-1, d)[:n].double(), v.view(-1, d)[:n].double()
+    k = torch.randint(0, 256, (pages, 1, page, d // 2), device="cuda", generator=gen, dtype=torch.uint8)
+    v = torch.randint(-2 ** 31, 2 ** 31 - 1, (pages, 1, page // 8, d), device="cuda", generator=gen, dtype=torch.int32)
+    km, vm = (torch.tensor([lo, 1 / 15], device="cuda").half().repeat(pages, 1, page, d // 64, 1) for lo in (-0.5, 0.5))
+    kc = torch.stack([k & 15, k >> 4], -1).reshape(-1, d)[:n]
+    vc = ((v.view(pages, page // 8, 1, d) >> (4 * torch.arange(8, device="cuda").view(8, 1))) & 15).reshape(-1, d)[:n]
+    value = lambda c, m: (c.float() * m[0, 0, 0, 0, 1].float() + m[0, 0, 0, 0, 0].float()).half().double()  # noqa: E731
+    return (k, v, km, vm), value(kc, km), value(vc, vm)
+
+
+def _long_history(bits, n, d, b, new, looked_at):
+    """Signed relative errors of `looked_at` rows of b sequences of `new` tokens that share one history
+    of n keys (the new tokens' among them)."""
+    page = 1024
+    bufs, k, v = _positive_pool(bits, n, d, page)
+    pages = bufs[0].shape[0]
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(b, 1).contiguous()
+    start = torch.arange(0, (b + 1) * new, new, dtype=torch.int32, device="cuda")
+    lens = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    cfg = fq.flexq_config(h=2 * d, heads=2, ffn=8 * d, w_bits=4, kv_bits=bits, ln_eps=1e-5)
+    kv = fq.flexq_paged_kv(*[t if t is None else t.data_ptr() for t in bufs], 1, pages, page, table.data_ptr(), pages)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    q = (0.3 * torch.randn(b * new, 2 * d, device="cuda", generator=gen)).half()
+    out = torch.full_like(q, float("nan"))
+    fq.flexq_attention_paged(cfg, kv, fq.flexq_ragged(b, b * new, new, n, start.data_ptr(), lens.data_ptr()), q, 2 * d, out,
+                             2 * d)
+    fq.flexq_device_status()
+    rows = torch.linspace(0, b * new - 1, looked_at, device="cuda").long()
+    s = q[rows].double().view(looked_at, 2, d) @ k.T / d ** 0.5
+    s.masked_fill_(torch.arange(n, device="cuda") > (n - new + rows % new)[:, None, None], float("-inf"))
+    ref = torch.softmax(s, -1) @ v
+    return (out[rows].double().view(looked_at, 2, d) / ref - 1).cpu().numpy()
+
+
+def check_drift(err):
+    """Each error is that of one output: its rounding to fp16 (2^-11), the weights' (2^-11 at the most)
+    and the sums' (2^-12), and a little for exponents of scores below 8 in size.  Their mean has
+    no roundings to fp16 in it, which go up as often as down (a mean of N of them is below
+    2^-11 * 4 / sqrt(3 N), four standard deviations, and the weights' are smaller still): what is left is what sums
+    lose or gain in one direction, 2^-13 at the most."""
+    assert np.abs(err).max() <= 2.0 ** -10 + 2.0 ** -12 + 2.0 ** -16, np.abs(err).max()
+    noise = 2 * 2.0 ** -11 * 4 / np.sqrt(3 * err.size)
+    assert abs(err.mean()) <= 2.0 ** -13 + noise, (err.mean(), noise)
+
+
+@pytest.mark.parametrize("bits,n,d,b", [(4, 262144, 128, 4800), (16, 200000, 64, 4800), (4, 16385, 64, 4800),
+                                        (4, 600000, 128, 3), (16, 17, 128, 300), (4, 300001, 64, 300)])
+def test_single_tokens_over_long_histories_do_not_drift(bits, n, d, b):
+    """Values of one sign, so that what a sum loses at each step shows; many sequences (few warps
+    a history) and few."""
+    check_drift(_long_history(bits, n, d, b, 1, min(b, 48)))
