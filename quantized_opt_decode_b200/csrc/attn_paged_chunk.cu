@@ -50,6 +50,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "warp_mma.cuh"
@@ -71,6 +72,11 @@ constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kLoadRegs = 80, kMmaRegs = 6
 static_assert(256 * kSoftmaxRegs + 256 * kLoadRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs,
               "a split above the launch's registers would wait for ever");
 constexpr int kMaxCluster = 8;
+// Key tiles that one accumulator takes.  The tensor core truncates, always towards zero, when it
+// adds to it: 1024 additions of at most 2^-23 each are a quarter of the output's own rounding, 2^-13
+// (measured over 16384 keys of values of one sign: 1.0e-4, and 3.8e-4 over 65536).  Where a CTA's share may
+// be longer, what has come together is put aside after every so many tiles and added up with rounding.
+constexpr int kShareTiles = 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
@@ -98,6 +104,8 @@ struct Layout {
   static constexpr int bytes = v0 + kStages * v_stage;
   static_assert(bytes - k0 >= kRows * D * 4, "the joined output lies over the K and V stages");
   static constexpr int smem = bytes + 1024;  // room to align the base
+  // joined output of a unit's pieces so far: 16 dimensions of a row a thread, its maximum and sum
+  static constexpr int kept = kRows * (16 + 2) * 4;
 };
 
 struct Barriers {
@@ -110,18 +118,20 @@ struct Barriers {
 // 256 query rows of one sequence and key/value head.
 struct Unit {
   int i, head, row0, first, len, c0, rows;
-  int tiles;   // key tiles that some row of the unit sees
-  bool joint;  // shared out over the cluster
+  int t0, tiles;  // key tiles t0 .. tiles - 1: the unit's, or the next piece of a shared-out one
+  int all;        // key tiles that some row of the unit sees
+  bool joint;     // shared out over the cluster
 };
 
 // The units of CTA (or cluster) `id` of `stride`, in order: one of each `stride` units, from the front
 // and from the back by turns (a sequence's later rows, which see more keys, come first).  A warp
 // counts the units of 32 sequences at a time, a lane each, as it comes to them; sequences that have none cost
 // nothing more.  In a launch of clusters first the cluster's units, those of joint_tiles tiles and
-// more, then the CTA's own, the shorter ones.
-template <bool J>
+// more, piece by piece, then the CTA's own, the shorter ones.
+template <bool J, bool P>
 struct UnitWalk {
   int id, stride, total;  // total: more units than a batch of sound spans has (any other ends there)
+  int most;               // tiles of a piece
   bool joint;
   int k, i0, before;      // units taken; the 32 sequences' first; units of the sequences before them
   int row0, n, len;       // the lane's sequence
@@ -130,6 +140,7 @@ struct UnitWalk {
   __device__ __forceinline__ void start(const ChunkArgs& a, int splits) {
     total = static_cast<int>(unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1));
     joint = J;
+    most = J && P ? kShareTiles * splits : 1 << 30;
     id = static_cast<int>(blockIdx.x) / splits;
     stride = static_cast<int>(gridDim.x) / splits;
     k = i0 = before = 0;
@@ -160,8 +171,13 @@ struct UnitWalk {
     }
     shift = skipped - (through - mine);
   }
-  // Every lane of the warp calls this and gets the same unit; false: no more.
+  // Every lane of the warp calls this, with the unit it got last, and gets the same unit; false: no more.
   __device__ __forceinline__ bool next(const ChunkArgs& a, Unit& out) {
+    if (J && P && out.joint && out.tiles < out.all) {
+      out.t0 = out.tiles;
+      out.tiles = min(out.all, out.t0 + most);
+      return true;
+    }
     int w, u;
     for (;;) {
       w = k * stride + (k & 1 ? stride - 1 - id : id);
@@ -197,8 +213,10 @@ struct UnitWalk {
     out.first = out.len - tokens;
     out.c0 = ((tokens * g + kRows - 1) / kRows - 1 - behind) * kRows;
     out.rows = min(kRows, tokens * g - out.c0);
-    out.tiles = (out.first + (out.c0 + out.rows - 1) / g + kKeys) / kKeys;
+    out.all = (out.first + (out.c0 + out.rows - 1) / g + kKeys) / kKeys;
     out.joint = J && joint;
+    out.t0 = 0;
+    out.tiles = J && P && out.joint ? min(out.all, most) : out.all;
     return true;
   }
 };
@@ -245,6 +263,12 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Load and wait in one statement.
@@ -484,8 +508,12 @@ struct Loader<D, false> {
   }
 };
 
-// J: in clusters, which share out long units.
-template <int D, bool Q4, bool J>
+// J: in clusters, which share out long units.  P: shares may be longer than kShareTiles.  A cluster then
+// takes a unit piece by piece and keeps the pieces' joined output; a CTA alone puts the bulk of O aside in the unit's
+// own rows of `out`, as fp16, and goes on with the remainder, which loses nothing.  (Forms of their own: what
+// they keep costs the softmax registers, 3240 us instead of 2850 for 148 chunks of 700 tokens over
+// 32768 keys shared out.)
+template <int D, bool Q4, bool J, bool P>
 __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const ChunkArgs a) {
   using L = Layout<D>;
   constexpr int W = Q4 ? 4 : 8;  // O's column (D / W) e + u is dimension W u + e
@@ -499,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   const int lane = static_cast<int>(lane_id());
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
   const int g = a.group;
-  UnitWalk<J> walk;
-  Unit un;
+  UnitWalk<J, P> walk;
+  Unit un{};
   walk.start(a, splits);
   const bool any = walk.next(a, un);
   if (blockIdx.x == 0 && warp == kMmaWarp + 1) check_spans(a.batch, a.err);
@@ -541,10 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
     return false;
   };
   // key tiles of this CTA: all, or rank, rank + splits, ..
-  auto first_of = [&](const Unit& x) { return J && x.joint ? rank : 0; };
+  auto start_of = [&](const Unit& x) { return J && P ? x.t0 : 0; };
+  auto first_of = [&](const Unit& x) { return J && x.joint ? start_of(x) + rank : 0; };
   auto step_of = [&](const Unit& x) { return J && x.joint ? splits : 1; };
   auto tiles_of = [&](const Unit& x) {
-    return !J || !x.joint ? x.tiles : x.tiles > rank ? (x.tiles - rank + splits - 1) / splits : 0;
+    return !J || !x.joint ? x.tiles : x.tiles - start_of(x) > rank ? (x.tiles - start_of(x) - rank + splits - 1) / splits : 0;
   };
   // A shared-out unit ends with two barriers of the whole cluster, which every warp passes whatever
   // became of its waits: parts are written before the first and read before the second.  No wait of a
@@ -610,10 +639,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       float limit = -INFINITY;  // the raw score that moves it
       uint64_t sum = 0;        // sums of the even and the odd columns' weights
       int lim = pos - first_of(cur) * kKeys;  // tokens 0 .. lim of the tile count
+      __half* dst = a.out + static_cast<size_t>(cur.row0 + tok) * a.ldo + (cur.head * g + c - tok * g) * D;
+      float unit = 0.f;  // of what is put aside in dst: O's columns (D / W) e + u0 .. + 7 at W u0 + 8 e .. + 7
+      auto put_aside = [&]() {
+        // |O| is at most the weights' sum times 65504 (and 2^-11 of that): with twice the sum's power of two
+        // as the unit it is in fp16's range.  Read, add, round, keep the remainder: all exact but the addition.
+        float s0, s1;
+        unpair(sum, s0, s1);
+        const int ex = (__float_as_int(s0 + s1) >> 23) - 127 + 2;
+        const float next = __int_as_float((ex + 127) << 23), inv = __int_as_float((127 - ex) << 23);
+#pragma unroll 1
+        for (int x0 = 0; x0 < D; x0 += 32) {  // 16-byte pieces of dst, four at a time
+          uint4 was[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            was[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (live && unit != 0.f) was[i] = *reinterpret_cast<const uint4*>(dst + x0 + 8 * i);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = x0 + 8 * i, col = (D / W) * (x / 8 % W) + x / (8 * W) * 8;
+            uint32_t o[8];
+            tmem_read_x8(o_col + col, o);
+            const uint32_t t[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
+            uint32_t to[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 w = __half22float2(as_half2(t[k]));
+              const float y0 = fmaf(w.x, unit, __uint_as_float(o[2 * k])), y1 = fmaf(w.y, unit, __uint_as_float(o[2 * k + 1]));
+              to[k] = pack_half2(y0 * inv, y1 * inv);
+              const float2 n = __half22float2(as_half2(to[k]));
+              o[2 * k] = __float_as_uint(fmaf(-n.x, next, y0));
+              o[2 * k + 1] = __float_as_uint(fmaf(-n.y, next, y1));
+            }
+            if (live) *reinterpret_cast<uint4*>(dst + x) = make_uint4(to[0], to[1], to[2], to[3]);
+            tmem_st_x8(o_col + col, o);
+          }
+        }
+        unit = next;
+        tmem_st_wait();
+      };
       for (int it = 0; it < mine; ++it, lim -= step_of(cur) * kKeys) {
         if (!(ok = __all_sync(0xffffffffu, wait(&bar.s_full[m], s_phase, DEV_TIMEOUT_EPILOGUE)))) break;
         s_phase ^= 1;
         tc_fence_after();
+        if (!J && P && it > 0 && it % kShareTiles == 0) put_aside();
         if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
           // the scores behind the row's position leave S here
 #pragma unroll 1
@@ -630,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
           }
           tmem_st_wait();
         }
-        uint64_t sums[4] = {sum, 0, 0, 0};
+        uint64_t sums[4] = {sum, 0, 0, 0};  // (17 roundings a tile: 2^-13 over kShareTiles at the most)
         uint32_t s[2][32];
         tmem_ld_x32(s_col, s[0]);
 #pragma unroll
@@ -652,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
             const float nb = top > limit ? ceilf(top * a.scale_log2) : base;
             const float alpha = base == -INFINITY ? 0.f : exp2_approx(base - nb);
             base = nb;
+            if (!J && P) unit *= alpha;
             limit = (nb + kWeightSlack) * inv_scale;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -713,13 +784,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         if (!(ok = __all_sync(0xffffffffu, wait(&bar.o_full[m], (o_phase >> m) & 1, DEV_TIMEOUT_EPILOGUE)))) break;
         tc_fence_after();
         const float inv = 1.f / (s0 + s1);
-        __half* dst = a.out + static_cast<size_t>(cur.row0 + tok) * a.ldo + (cur.head * g + c - tok * g) * D;
 #pragma unroll 1
         for (int u0 = 0; u0 < D / W; u0 += 8) {
           uint32_t o[W][8];
 #pragma unroll
           for (int e = 0; e < W; ++e) tmem_read_x8(o_col + (D / W) * e + u0, o[e]);
           if (live) {
+            if (!J && P && cur.all > kShareTiles) {
+#pragma unroll
+              for (int e = 0; e < W; ++e) {
+                const uint4 was = *reinterpret_cast<const uint4*>(dst + W * u0 + 8 * e);
+                const uint32_t* t = reinterpret_cast<const uint32_t*>(&was);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 w = __half22float2(as_half2(t[i]));
+                  o[e][2 * i] = __float_as_uint(fmaf(w.x, unit, __uint_as_float(o[e][2 * i])));
+                  o[e][2 * i + 1] = __float_as_uint(fmaf(w.y, unit, __uint_as_float(o[e][2 * i + 1])));
+                }
+              }
+            }
 #pragma unroll
             for (int x = 0; x < 8 * W; x += 8) {
               uint32_t h[4];
@@ -762,53 +845,77 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
         }
         cluster_sync();
         const bool fine = cluster_fine();
-        // join the cluster's parts, 4 W dimensions of a row at a time: columns u .. u + 3 of O's W stretches
-        constexpr int items = D / (4 * W), C4 = D / 4;
+        // join the cluster's parts, N dimensions of a row at a time: C columns of each of O's W
+        // stretches.  Where the unit goes on, the thread keeps what it has and takes it up again: pieces
+        // are only of clusters of eight, where nobody has more than one item.
+        constexpr int C = P ? 16 / W : 4, N = C * W, items = D / N;
+        static_assert(!P || items <= kMaxCluster, "one item a thread");
+        using Cols = typename std::conditional<C == 4, float4, float2>::type;
         // (an aligned base is at the same offset in every CTA of the launch)
-        const float4* parts = reinterpret_cast<const float4*>(smem + L::k0);
+        const float* parts = reinterpret_cast<const float*>(smem + L::k0);
+        float4* kept = reinterpret_cast<float4*>(smem + L::bytes) + threadIdx.x;
+        float* kept_m = reinterpret_cast<float*>(smem + L::bytes + kRows * 64) + threadIdx.x;
+        const bool goes_on = P && cur.tiles < cur.all, resumed = P && cur.t0 > 0;
 #pragma unroll 1
         for (int x = rank * kRows + static_cast<int>(threadIdx.x); fine && x < items * kRows; x += splits * kRows) {
-          const int jr = x % kRows, u4 = x / kRows;
+          const int jr = x % kRows, u = x / kRows;
           if (jr >= cur.rows) break;
-          float f[kMaxCluster], top = -INFINITY, den = 0.f;
+          float f[kMaxCluster], top = -INFINITY, den = 0.f, back = 0.f;
 #pragma unroll
           for (int k = 0; k < kMaxCluster; ++k) {
             f[k] = k < splits ? *cluster.map_shared_rank(&s_m[jr], k) : -INFINITY;
             top = fmaxf(top, f[k]);
+          }
+          if (resumed) {
+            const float m0 = kept_m[0];  // (finite: every row sees the first tile)
+            top = fmaxf(top, m0);
+            back = exp2_approx(m0 - top);
+            den = back * kept_m[kRows];
           }
 #pragma unroll
           for (int k = 0; k < kMaxCluster; ++k) {
             f[k] = f[k] == -INFINITY ? 0.f : exp2_approx(f[k] - top);
             if (k < splits) den += f[k] * *cluster.map_shared_rank(&s_l[jr], k);
           }
-          const float inv = 1.f / den;
-          float o[W][4];
+          float o[N];
+#pragma unroll
+          for (int q = 0; q < N / 4; ++q) {
+            const float4 was = resumed ? kept[q * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[4 * q] = back * was.x;
+            o[4 * q + 1] = back * was.y;
+            o[4 * q + 2] = back * was.z;
+            o[4 * q + 3] = back * was.w;
+          }
 #pragma unroll
           for (int q = 0; q < W; ++q) {
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float* at = parts + jr * D + ((((q * (D / W) + C * u) >> 2) ^ (jr & 7)) << 2) + ((C * u) & 3);
 #pragma unroll
             for (int k = 0; k < kMaxCluster; ++k) {
               if (k >= splits) continue;
-              const float4 pk = *cluster.map_shared_rank(parts + jr * C4 + ((q * items + u4) ^ (jr & 7)), k);
-              acc.x += f[k] * pk.x;
-              acc.y += f[k] * pk.y;
-              acc.z += f[k] * pk.z;
-              acc.w += f[k] * pk.w;
-            }
-            o[q][0] = acc.x * inv;
-            o[q][1] = acc.y * inv;
-            o[q][2] = acc.z * inv;
-            o[q][3] = acc.w * inv;
-          }
-          const int jc = cur.c0 + jr;
-          __half* dst = a.out + static_cast<size_t>(cur.row0 + jc / g) * a.ldo + (cur.head * g + jc % g) * D + u4 * (4 * W);
+              const Cols pk = *reinterpret_cast<const Cols*>(cluster.map_shared_rank(at, k));
+              const float* e = reinterpret_cast<const float*>(&pk);
 #pragma unroll
-          for (int e = 0; e < 4 * W; e += 8)  // dimension e of these: stretch e % W, column e / W
-            *reinterpret_cast<uint4*>(dst + e) =
-                make_uint4(pack_half2(o[e % W][e / W], o[(e + 1) % W][(e + 1) / W]),
-                           pack_half2(o[(e + 2) % W][(e + 2) / W], o[(e + 3) % W][(e + 3) / W]),
-                           pack_half2(o[(e + 4) % W][(e + 4) / W], o[(e + 5) % W][(e + 5) / W]),
-                           pack_half2(o[(e + 6) % W][(e + 6) / W], o[(e + 7) % W][(e + 7) / W]));
+              for (int c = 0; c < C; ++c) o[q * C + c] += f[k] * e[c];
+            }
+          }
+          if (goes_on) {
+            kept_m[0] = top;
+            kept_m[kRows] = den;
+#pragma unroll
+            for (int q = 0; q < N / 4; ++q) kept[q * kRows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            continue;
+          }
+          const float inv = 1.f / den;
+          const int jc = cur.c0 + jr;
+          __half* dst = a.out + static_cast<size_t>(cur.row0 + jc / g) * a.ldo + (cur.head * g + jc % g) * D + u * N;
+#pragma unroll
+          for (int e = 0; e < N; e += 8) {  // dimension e of these: stretch e % W, column e / W
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+              h[i / 2] = pack_half2(o[(e + i) % W * C + (e + i) / W] * inv, o[(e + i + 1) % W * C + (e + i + 1) / W] * inv);
+            *reinterpret_cast<uint4*>(dst + e) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
         }
         cluster_sync();  // nobody writes, or leaves, while another reads its shared memory
         if (!fine) break;
@@ -969,20 +1076,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool Q4, bool J>
+template <int D, bool Q4, bool J, bool P>
 cudaError_t launch_j(const ChunkArgs& a, long long works, int splits, cudaStream_t s) {
-  cudaError_t e = allow_smem<attn_paged_chunk_kernel<D, Q4, J>>(Layout<D>::smem);
+  constexpr int smem = Layout<D>::smem + (J && P ? Layout<D>::kept : 0);
+  cudaError_t e = allow_smem<attn_paged_chunk_kernel<D, Q4, J, P>>(smem);
   if (e != cudaSuccess) return e;
   // the split of the registers counts on the launch having them
   static const int regs = [] {
     cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, attn_paged_chunk_kernel<D, Q4, J>) == cudaSuccess ? f.numRegs : 0;
+    return cudaFuncGetAttributes(&f, attn_paged_chunk_kernel<D, Q4, J, P>) == cudaSuccess ? f.numRegs : 0;
   }();
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(splits));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<D>::smem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -996,12 +1104,12 @@ cudaError_t launch_j(const ChunkArgs& a, long long works, int splits, cudaStream
   static std::atomic<int> resident[kMaxCluster + 1];
   int clusters = J ? resident[splits].load(std::memory_order_relaxed) : runtime().num_sms;
   if (clusters == 0) {
-    if ((e = cudaOccupancyMaxActiveClusters(&clusters, attn_paged_chunk_kernel<D, Q4, J>, &cfg)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, attn_paged_chunk_kernel<D, Q4, J, P>, &cfg)) != cudaSuccess) return e;
     clusters = std::max(clusters, 1);
     resident[splits].store(clusters, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(works, clusters) * splits));
-  e = cudaLaunchKernelEx(&cfg, attn_paged_chunk_kernel<D, Q4, J>, a);
+  e = cudaLaunchKernelEx(&cfg, attn_paged_chunk_kernel<D, Q4, J, P>, a);
   return e != cudaSuccess ? e : launched();
 }
 
@@ -1020,7 +1128,11 @@ cudaError_t launch_d(const ChunkArgs& args, cudaStream_t s) {
   ChunkArgs a = args;
   a.joint_tiles = splits > 1 ? 2 * splits : 48;
   while (splits < kMaxCluster && full < 4ll * sms && args.batch.max_len / (2 * splits) >= 32 * kKeys) splits *= 2;
-  return splits > 1 ? launch_j<D, Q4, true>(a, works, splits, s) : launch_j<D, Q4, false>(a, works, 1, s);
+  // (clusters: no share longer than an accumulator takes, as far as their size goes)
+  while (splits > 1 && splits < kMaxCluster && args.batch.max_len > splits * kShareTiles * kKeys) splits *= 2;
+  const bool pieces = args.batch.max_len > splits * kShareTiles * kKeys;
+  if (splits == 1) return pieces ? launch_j<D, Q4, false, true>(a, works, 1, s) : launch_j<D, Q4, false, false>(a, works, 1, s);
+  return pieces ? launch_j<D, Q4, true, true>(a, works, splits, s) : launch_j<D, Q4, true, false>(a, works, splits, s);
 }
 
 }  // namespace

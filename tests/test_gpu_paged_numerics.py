@@ -181,3 +181,96 @@ def test_single_tokens_over_long_histories_do_not_drift(bits, n, d, b):
     """Values of one sign, so that what a sum loses at each step shows; many sequences (few warps
     a history) and few."""
     check_drift(_long_history(bits, n, d, b, 1, min(b, 48)))
+
+
+CHUNKS = [  # bits, keys, d, sequences, new tokens
+    (4, 16384, 128, 3, 150), (4, 16385, 64, 160, 130), (16, 30000, 128, 300, 64), (16, 40000, 64, 2, 40),
+    (4, 65537, 128, 90, 140), (4, 131072, 64, 2, 129), (16, 131073, 128, 1, 20), (4, 131082, 128, 2, 30),
+    (4, 140000, 128, 20, 300), (16, 300000, 64, 1, 9), (4, 530000, 128, 1, 40), (4, 40000, 128, 160, 512),
+    (16, 33000, 64, 170, 480), (4, 16500, 64, 200, 400)]
+
+
+@pytest.mark.parametrize("bits,n,d,b,new", CHUNKS)
+def test_chunks_over_long_histories_do_not_drift(bits, n, d, b, new):
+    """The same for chunks: histories that one accumulator takes, that a cluster does, that it takes in
+    pieces, the last of which some rows see nothing of, and that each of many CTAs takes alone."""
+    check_drift(_long_history(bits, n, d, b, new, 48))
+
+
+@pytest.mark.parametrize("bits,d", [(4, 128), (16, 64)])
+def test_pieces_of_a_history_with_different_bases(bits, d):
+    """Scores that grow and fall from piece to piece of 131072 keys, each of which counts."""
+    n, new = 300000, 24
+    pg = ph.Paged(bits, 1, 1, d, 1024, (new,), (n - new,), seed=2, spare=1) if d == 128 else \
+        ph.Paged(bits, 2, 1, d, 1024, (new,), (n - new,), seed=2, spare=1)
+    for level, boost in (((0, 9, 15), (9, 0, 0)), ((20, 0, 9), (0, 12, 3)), ((0, 3, -6), (0, 0, 4))):
+        piece = np.minimum(np.arange(n) // 131072, 2)
+        set_levels(pg, 0, (np.array(level, float)[piece] / np.log2(np.e) / np.sqrt(d)).astype(np.float16), np.array(boost)[piece])
+        dv = Dev(pg)
+        q = np.ones((new, pg.heads * d), np.float16)
+        q[::3] *= -0.5
+        out = torch.full((new, pg.heads * d), float("nan"), dtype=torch.float16, device="cuda")
+        fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), pg.heads * d, out, pg.heads * d)
+        fq.flexq_device_status()
+        k, v = pg.history(0)
+        ref, tol = attention_rows(q[:, :d], k[:, 0], v[:, 0], n - new)
+        over = np.abs(to_host(out)[:, :d].astype(np.float64) - ref) / tol
+        assert over.max() <= 1, (level, over.max())
+        set_levels(pg, 0, np.zeros(n), -np.array(boost)[piece])
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_long_histories_of_many_units_with_different_bases(bits):
+    """The same where the units are many and each is one CTA's: scores that grow and fall every 16384
+    keys, by more than fp32's range too, values that make up for it, and a bound far above the batch."""
+    n, new, d, heads = 40000, 2400, 64, 64
+    pg = ph.Paged(bits, heads, 1, d, 1024, (new,), (n - new,), seed=3, spare=1)
+    pg.table = np.concatenate([pg.table, np.full((1, 100), -1, np.int32)], 1)
+    pg.table_ld = pg.table.shape[1]
+    rows = [0, 1, 2, 255, 256, 700, 1600, 1601, new - 1]
+    for level, boost in (((0, 9, 15), (9, 0, 0)), ((20, 0, 9), (0, 12, 3)), ((0, 3, -6), (0, 0, 4)), ((0, 140, 131), (0, 0, 9)),
+                         ((150, 0, 0), (0, 0, 0))):
+        piece = np.minimum(np.arange(n) // 16384, 2)
+        set_levels(pg, 0, (np.array(level, float)[piece] / np.log2(np.e) / np.sqrt(d)).astype(np.float16), np.array(boost)[piece])
+        dv = Dev(pg, max_len=100000)
+        q = np.ones((new, heads * d), np.float16)
+        q[::3] *= -0.5
+        out = torch.full((new, heads * d), float("nan"), dtype=torch.float16, device="cuda")
+        fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), heads * d, out, heads * d)
+        fq.flexq_device_status()
+        out = to_host(out).astype(np.float64).reshape(new, heads, d)
+        assert (out == out[:, :1]).all()  # (the heads' queries are alike)
+        k, v = pg.history(0)
+        for t in rows:
+            ref, tol = attention_rows(q[t:t + 1, :d], k[:, 0], v[:, 0], n - new + t)
+            over = np.abs(out[t, 0] - ref[0]) / tol[0]
+            assert over.max() <= 1, (level, t, over.max())
+        set_levels(pg, 0, np.zeros(n), -np.array(boost)[piece])
+
+
+def test_a_wait_that_runs_out_in_a_piece_is_reported_and_the_next_call_is_right():
+    n, new, d, page = 270000, 20, 64, 1024
+    bufs, k, v = _positive_pool(4, n, d, page)
+    pages = bufs[0].shape[0]
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")
+    start, lens = to_dev(np.array([0, new], np.int32)), to_dev(np.array([n], np.int32))
+    cfg = fq.flexq_config(h=2 * d, heads=2, ffn=8 * d, w_bits=4, kv_bits=4, ln_eps=1e-5)
+    kv = fq.flexq_paged_kv(*[t.data_ptr() for t in bufs], 1, pages, page, table.data_ptr(), pages)
+    q = torch.randn(new, 2 * d, device="cuda").half()
+    outs = [torch.full_like(q, float("nan")) for _ in range(2)]
+
+    def run(out):
+        fq.flexq_attention_paged(cfg, kv, fq.flexq_ragged(1, new, new, n, start.data_ptr(), lens.data_ptr()), q, 2 * d, out, 2 * d)
+    run(outs[0])
+    fq.flexq_device_status()
+    try:
+        fq.flexq_set_wait_limit_ns(1)
+        run(outs[1])
+        with pytest.raises(fq.FlexqError) as ei:
+            fq.flexq_device_status()
+        assert ei.value.status == 4
+    finally:
+        fq.flexq_set_wait_limit_ns(0)
+    run(outs[1])
+    fq.flexq_device_status()
+    np.testing.assert_array_equal(to_host(outs[0]).view(np.uint16), to_host(outs[1]).view(np.uint16))
