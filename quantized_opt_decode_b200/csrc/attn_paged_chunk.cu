@@ -49,10 +49,10 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "paged.cuh"
+#include "per_device.h"
 #include "warp_mma.cuh"
 
 namespace flexq {
@@ -1081,11 +1081,17 @@ cudaError_t launch_j(const ChunkArgs& a, long long works, int splits, cudaStream
   constexpr int smem = Layout<D>::smem + (J && P ? Layout<D>::kept : 0);
   cudaError_t e = allow_smem<attn_paged_chunk_kernel<D, Q4, J, P>>(smem);
   if (e != cudaSuccess) return e;
+  int dev = 0, regs = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   // the split of the registers counts on the launch having them
-  static const int regs = [] {
+  static PerDevice registers;
+  e = registers.get(dev, &regs, [](int* n) {
     cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, attn_paged_chunk_kernel<D, Q4, J, P>) == cudaSuccess ? f.numRegs : 0;
-  }();
+    const cudaError_t err = cudaFuncGetAttributes(&f, attn_paged_chunk_kernel<D, Q4, J, P>);
+    *n = f.numRegs;
+    return err;
+  });
+  if (e != cudaSuccess) return e;
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(splits));
@@ -1101,12 +1107,15 @@ cudaError_t launch_j(const ChunkArgs& a, long long works, int splits, cudaStream
   cfg.attrs = attr;
   cfg.numAttrs = runtime().pdl ? 2 : 1;
   // one CTA an SM, or as many clusters as are resident at once
-  static std::atomic<int> resident[kMaxCluster + 1];
-  int clusters = J ? resident[splits].load(std::memory_order_relaxed) : runtime().num_sms;
-  if (clusters == 0) {
-    if ((e = cudaOccupancyMaxActiveClusters(&clusters, attn_paged_chunk_kernel<D, Q4, J, P>, &cfg)) != cudaSuccess) return e;
-    clusters = std::max(clusters, 1);
-    resident[splits].store(clusters, std::memory_order_relaxed);
+  static PerDevice resident[kMaxCluster + 1];
+  int clusters = runtime().num_sms;
+  if (J) {
+    e = resident[splits].get(dev, &clusters, [&cfg](int* n) {
+      const cudaError_t err = cudaOccupancyMaxActiveClusters(n, attn_paged_chunk_kernel<D, Q4, J, P>, &cfg);
+      *n = std::max(*n, 1);
+      return err;
+    });
+    if (e != cudaSuccess) return e;
   }
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(works, clusters) * splits));
   e = cudaLaunchKernelEx(&cfg, attn_paged_chunk_kernel<D, Q4, J, P>, a);
