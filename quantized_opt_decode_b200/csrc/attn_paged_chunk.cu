@@ -60,9 +60,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kRowShift = 8;  // 256 query rows of a unit
-constexpr int kRows = 1 << kRowShift;
-constexpr int kKeys = 128;
+constexpr int kRows = kUnitRows;  // 256 query rows of a unit
+constexpr int kKeys = kKeyTile;
 constexpr int kStages = 2;
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
@@ -83,7 +82,7 @@ constexpr uint64_t kDrainNs = 2000000000ull;
 struct ChunkArgs {
   PagedView kv;
   RaggedView batch;
-  int heads, group;
+  int group;
   int min_rows;
   int joint_tiles;  // tiles from which on a unit is shared out
   const __half* q;
@@ -138,7 +137,7 @@ struct UnitWalk {
   int through, shift;     // units of the sequences up to and with it; minus the first one's number
 
   __device__ __forceinline__ void start(const ChunkArgs& a, int splits) {
-    total = static_cast<int>(unit_total(a.batch.rows, a.batch.b, a.group, kRowShift, 1));
+    total = static_cast<int>(unit_total(a.batch.rows, a.batch.b, a.group, kUnitRowShift, 1));
     joint = J;
     most = J && P ? kShareTiles * splits : 1 << 30;
     id = static_cast<int>(blockIdx.x) / splits;
@@ -154,12 +153,10 @@ struct UnitWalk {
     n = sp.n;
     len = sp.len;
     const int rows = n * a.group;  // at most max_new * group, which the entry point bounds
-    const int units = n > 0 && rows >= a.min_rows ? (rows + kRows - 1) / kRows : 0;
+    const int units = n > 0 && rows >= a.min_rows ? row_units(rows) : 0;
     int mine = units, skipped = 0;
     if (J) {
-      // long ones: the last row's token is at or behind `need`
-      const int need = kKeys * (a.joint_tiles - 1) - (len - n);
-      const int longs = units == 0 || need >= n ? 0 : need <= 0 ? units : units - need * a.group / kRows;
+      const int longs = long_units(len - n, n, a.group, units, a.joint_tiles);
       mine = joint ? longs : units - longs;
       skipped = joint ? 0 : longs;
     }
@@ -211,9 +208,9 @@ struct UnitWalk {
     const int tokens = __shfl_sync(0xffffffffu, n, from);
     const int behind = u - before + __shfl_sync(0xffffffffu, shift, from);  // units of later rows
     out.first = out.len - tokens;
-    out.c0 = ((tokens * g + kRows - 1) / kRows - 1 - behind) * kRows;
-    out.rows = min(kRows, tokens * g - out.c0);
-    out.all = (out.first + (out.c0 + out.rows - 1) / g + kKeys) / kKeys;
+    out.c0 = (row_units(tokens * g) - 1 - behind) * kRows;
+    out.rows = unit_rows(tokens * g, out.c0);
+    out.all = unit_tiles(out.first, g, out.c0, out.rows);
     out.joint = J && joint;
     out.t0 = 0;
     out.tiles = J && P && out.joint ? min(out.all, most) : out.all;
@@ -573,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
   auto first_of = [&](const Unit& x) { return J && x.joint ? start_of(x) + rank : 0; };
   auto step_of = [&](const Unit& x) { return J && x.joint ? splits : 1; };
   auto tiles_of = [&](const Unit& x) {
-    return !J || !x.joint ? x.tiles : x.tiles - start_of(x) > rank ? (x.tiles - start_of(x) - rank + splits - 1) / splits : 0;
+    return !J || !x.joint ? x.tiles : share_tiles(x.tiles - start_of(x), rank, splits);
   };
   // A shared-out unit ends with two barriers of the whole cluster, which every warp passes whatever
   // became of its waits: parts are written before the first and read before the second.  No wait of a
@@ -1125,7 +1122,7 @@ cudaError_t launch_j(const ChunkArgs& a, long long works, int splits, cudaStream
 template <int D, bool Q4>
 cudaError_t launch_d(const ChunkArgs& args, cudaStream_t s) {
   const int sms = runtime().num_sms;
-  const long long works = unit_total(args.batch.rows, args.batch.b, args.group, kRowShift, 1) * args.kv.kv_heads;
+  const long long works = unit_total(args.batch.rows, args.batch.b, args.group, kUnitRowShift, 1) * args.kv.kv_heads;
   // Units that the batch's rows fill.  Histories are shared out while that leaves SMs idle and every
   // CTA keeps two tiles of keys; and, while an SM has few units, very long ones too, into shares
   // of 32 tiles and more: the longest unit's CTA would work on alone (12 sequences of up to 24000 keys,
@@ -1148,7 +1145,7 @@ cudaError_t launch_d(const ChunkArgs& args, cudaStream_t s) {
 
 cudaError_t launch_attn_paged_chunks(const PagedView& kv, const RaggedView& batch, int heads, int d, int kv_bits,
                                      int min_rows, const __half* q, int ldq, __half* out, int ldo, cudaStream_t s) {
-  const ChunkArgs a{kv, batch, heads, heads / kv.kv_heads, min_rows, 0, q, ldq, out, ldo,
+  const ChunkArgs a{kv, batch, heads / kv.kv_heads, min_rows, 0, q, ldq, out, ldo,
                     1.4426950408889634f / sqrtf(static_cast<float>(d)), runtime().wait_limit_ns, runtime().err};
   if (kv_bits == 4) return d == 128 ? launch_d<128, true>(a, s) : launch_d<64, true>(a, s);
   return d == 128 ? launch_d<128, false>(a, s) : launch_d<64, false>(a, s);

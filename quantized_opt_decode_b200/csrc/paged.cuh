@@ -35,26 +35,27 @@ __device__ __forceinline__ void check_spans(const RaggedView& r, uint32_t* err) 
   for (int i = static_cast<int>(lane_id()); i < r.b; i += 32) ragged_span(r, i, err);
 }
 
-__device__ __forceinline__ long long unit_base(const RaggedView& r, int i, int scale, int shift, int extra) {
-  return unit_base_at(r.row_start[i], i, scale, shift, extra);
+// First unit of 2^shift rows of sequence i.
+__device__ __forceinline__ long long unit_base(const RaggedView& r, int i, int shift, int extra) {
+  return unit_base_at(r.row_start[i], i, 1, shift, extra);
 }
 
 // Sequence that owns unit u: the last i in 0 .. b-1 with unit_base(i) <= u,
 // found 32 probes at a time by the whole warp.  -1: none.
-__device__ __forceinline__ int find_unit_owner(const RaggedView& r, long long u, int scale, int shift, int extra) {
+__device__ __forceinline__ int find_unit_owner(const RaggedView& r, long long u, int shift, int extra) {
   const int lane = static_cast<int>(lane_id());
   int lo = 0, hi = r.b;  // the owner, if any, is in [lo, hi)
   while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32;
     const int p = lo + lane * step;
-    const bool le = p < hi && unit_base(r, p, scale, shift, extra) <= u;
+    const bool le = p < hi && unit_base(r, p, shift, extra) <= u;
     const int cnt = __popc(__ballot_sync(0xffffffffu, le));
     if (cnt == 0) return -1;
     lo += (cnt - 1) * step;
     hi = min(hi, lo + step);
   }
   const int p = lo + lane;
-  const bool le = p < hi && unit_base(r, p, scale, shift, extra) <= u;
+  const bool le = p < hi && unit_base(r, p, shift, extra) <= u;
   const int cnt = __popc(__ballot_sync(0xffffffffu, le));
   return cnt == 0 ? -1 : lo + cnt - 1;
 }

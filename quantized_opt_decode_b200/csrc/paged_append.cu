@@ -233,9 +233,9 @@ __device__ __forceinline__ bool find_unit(const RaggedView& batch, int u, Unit& 
   if (batch.max_new == 1) {  // one block per sequence
     w.i = u;
   } else {
-    w.i = find_unit_owner(batch, u, 1, kUnitShift, kUnitExtra);
+    w.i = find_unit_owner(batch, u, kUnitShift, kUnitExtra);
     if (w.i < 0) return false;
-    blk_rel = u - static_cast<int>(unit_base(batch, w.i, 1, kUnitShift, kUnitExtra));
+    blk_rel = u - static_cast<int>(unit_base(batch, w.i, kUnitShift, kUnitExtra));
   }
   const Span sp = ragged_span(batch, w.i, err);
   if (sp.n == 0) return false;

@@ -36,4 +36,29 @@ FQ_HD long long unit_total(int rows, int b, int scale, int shift, int extra) {
   return ((static_cast<long long>(rows) * scale) >> shift) + static_cast<long long>(extra) * b;
 }
 
+// The chunk kernel's units: kUnitRows consecutive query rows of a sequence and key/value head (rows = n
+// new tokens times `group` query heads, at most 2^30), and the key tiles that they see.
+// `first` is the position of the first new token.
+constexpr int kUnitRowShift = 8;
+constexpr int kUnitRows = 1 << kUnitRowShift;
+constexpr int kKeyTile = 128;
+
+FQ_HD int row_units(int rows) { return (rows + kUnitRows - 1) / kUnitRows; }
+
+// Rows of the unit that starts at row c0.
+FQ_HD int unit_rows(int rows, int c0) { return rows - c0 < kUnitRows ? rows - c0 : kUnitRows; }
+
+// Key tiles that its last row sees.
+FQ_HD int unit_tiles(int first, int group, int c0, int rows) { return (first + (c0 + rows - 1) / group + kKeyTile) / kKeyTile; }
+
+// How many of the `units` of a sequence of n new tokens (no units: it is not the kernel's) see at
+// least `tiles` (> 0) tiles: its last ones, from the row on whose token is at or behind `need`.
+FQ_HD int long_units(int first, int n, int group, int units, int tiles) {
+  const int need = kKeyTile * (tiles - 1) - first;
+  return units == 0 || need >= n ? 0 : need <= 0 ? units : units - need * group / kUnitRows;
+}
+
+// How many of `tiles` tiles fall to CTA `rank` of a cluster of `splits`: rank, rank + splits, ..
+FQ_HD int share_tiles(int tiles, int rank, int splits) { return tiles > rank ? (tiles - rank + splits - 1) / splits : 0; }
+
 }  // namespace flexq
