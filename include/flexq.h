@@ -175,8 +175,9 @@ flexq_status flexq_linear_static_scratch(const void* x_dev, int ldx, const void*
 
 /* flexq_linear for a few rows (1 <= m <= 16) and a 4-bit weight: the products
  * of a step over one to sixteen sequences, where reading the weight once is the
- * whole cost.  w_dev: the tiled layout of flexq_packed_weight_bytes, used with
- * flexq_linear's arithmetic (w = fp16(fp32(code * scale) + min), fp32 sums) and
+ * whole cost; flexq_linear takes the same calls, and longer for them.  w_dev: the
+ * tiled layout of flexq_packed_weight_bytes, used with
+ * flexq_linear's arithmetic (w = code * scale + min rounded once to fp16, fp32 sums) and
  * flexq_linear's epilogue flags; the two differ only in the order of the sums.
  * x_dev fp16 [m][ldx] (ldx >= k, ldx % 8 == 0), residual_dev fp16 [m][ld_res],
  * y_dev fp16 [m][ldy], or fp32 with flag 8.  y may be residual (same
@@ -377,10 +378,11 @@ flexq_status flexq_paged_read(const flexq_config* cfg, const flexq_paged_kv* kv,
 /* Attention of the new tokens over the paged cache, their own slots included
  * (append first): the row at position p attends over positions 0..p,
  * out[row][j*d ..] = softmax(q K^T / sqrt(d)) V with the cache's fp16
- * values (4-bit: the dequantized codes).  q_dev fp16 [rows][ldq], out_dev fp16
+ * values (4-bit: code * scale + min rounded once to fp16; flexq_paged_read's values, but for those
+ * whose first rounding to fp32 makes a tie).  q_dev fp16 [rows][ldq], out_dev fp16
  * [rows][ldo], not over q.  Chunks of a prompt, single tokens, and both in one
  * batch: sequences with up to 8 (or 16) query rows to a key/value head take a form that reads
- * the cache at its bandwidth, the others one that multiplies on the tensor core's
+ * the cache once, the others one that multiplies on the tensor core's
  * accumulator memory; a batch that may hold both is two launches.  Scores, the softmax's
  * maximum and sum and the output are held in fp32; the weights enter the
  * product with V in fp16, unnormalised (a weight below 2^-21 of its row's largest to within 2^-31 of

@@ -18,13 +18,16 @@
 // output) are joined in a fixed order: in shared memory, then over the cluster's
 // distributed shared memory, so the call needs no workspace.
 //
-// Measured (B200): 144 sequences of 300 to 1040 keys, 56 heads, d = 128, 4 bit: 201 to 214 us from box to
-// box for 788 MB, 0.57 to 0.60 of the copy rate; five of 18900 to 32700 keys, 8 key/value heads: 58 us for
+// Measured (B200): 144 sequences of 300 to 1040 keys, 56 heads, d = 128, 4 bit: 200 to 214 us from box to
+// box for 788 MB, 0.57 to 0.60 of the copy rate; five of 18900 to 32700 keys, 8 key/value heads: 58 to 61 us for
 // 149 MB (the clusters are alike, the histories are not: the longest is 1.3 times the mean); one fp16
-// sequence of 902 keys, 32 heads, d = 64: 5.8 us, the launch.  The 4-bit form is bound by the half-precision
-// pipe that the dequantizer's eight multiply-adds and the mma.sync of a word share: 23 cycles a
-// word and scheduler alone in a loop, 750 cycles a tile of the 1150 that it takes.  Three quarters of
-// the registers (18 warps an SM) gained nothing (214 us), nor did two stages instead of three.
+// sequence of 902 keys, 32 heads, d = 64: 5.8 us, the launch.  The 4-bit form has no unit at its
+// roof.  Closest is the half-precision pipe that the dequantizer's eight multiply-adds and the mma.sync of
+// a word share: 23 cycles a word and scheduler alone in a loop, 750 cycles a tile of the 1150 that it takes,
+// and by itself it would allow nearly the copy rate.  The rest is what a warp does in sequence (dequantize K,
+// products, maximum, exponentials, transpose, dequantize V, products) with 13 warps an SM to overlap it.
+// Three quarters of the registers (18 warps an SM) gained nothing (214 us), nor did two stages instead of
+// three.  An fp16 cache has no dequantizer: 64 sequences of 528 keys, 32 heads, d = 128, read at 6.2 TB/s.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -532,9 +535,11 @@ __global__ void __maxnreg__(NT == 1 ? 128 : 168) attn_paged_rows_kernel(const Pa
 }
 
 // How a unit's history is dealt out: warps of a CTA and CTAs of a cluster (its tiles go round
-// them all).  An SM holds 16 warps.  Very many units: two warps each, so that the fixed cost of a
+// them all).  The plan counts on 16 warps an SM, which is what eight columns of a 4-bit cache, or of fp16 with
+// d = 64, have; with sixteen columns 12 warps fit (registers), with fp16 and d = 128 nine (rings), and a launch that
+// is meant to be resident at once then takes two rounds.  Very many units: two warps each, so that the fixed cost of a
 // unit is shared by few (8064 units of 300 to 1040 keys: 205 us with two, 211 with four, 231 with one).  Few
-// units: the largest number of warps that is resident at once.  Where that leaves a fifth of the SMs'
+// units: the largest number of warps that is resident at once, by that count.  Where that leaves a fifth of the SMs'
 // room empty and histories are long, four-warp CTAs in at least two and a half rounds, down to
 // 512 keys a CTA (320 units of 8000 keys: 118 us in one round of 320 CTAs).
 struct Plan {

@@ -13,8 +13,9 @@
 //                    are read once, 32 columns at a time, and where the base moves, the factor
 //                    for O and for the P already stored is exact (kWeightBias: what P is in fp16);
 //   warps 8-15       bring K and V: pages looked up two tiles ahead, codes fetched one
-//                    tile ahead into registers, dequantized (rounded once to fp16, as the codec's
-//                    values) and stored in the 128-byte-swizzled layout; a
+//                    tile ahead into registers (of an fp16 cache only once its stage is free: 363 us
+//                    where the 4-bit form takes 395), dequantized (code * scale + min rounded
+//                    once to fp16) and stored in the 128-byte-swizzled layout; a
 //                    word of codes is one 16-byte store, since the orders of the head's
 //                    dimensions in Q K^T, of the keys in P V and of O's columns are
 //                    free: pairs (e, e + 4) of Q are swapped into place when Q is
@@ -43,8 +44,9 @@
 // then run at the same time); a quarter of the exponentials as polynomials (446 us: issue slots);
 // loops rolled up for the instruction cache (519 us); four loading warps (446 us); the largest score of the
 // whole tile first, P then handed over in halves (447 us: scores are read twice); two key tiles at once
-// for units of one row tile (434 us); pages' entries looked at a step after their load (423 us).  The
-// roles' waits are inlined: a function call would tie the roles to one register count.
+// for units of one row tile (434 us); pages' entries looked at a step after their load (423 us).  The softmax
+// keeps more than its registers hold: 156 to 260 bytes of spill stores a thread without clusters, 900 to
+// 1050 with them.  The roles' waits are inlined: a function call would tie the roles to one register count.
 #include <cooperative_groups.h>
 #include <math.h>
 

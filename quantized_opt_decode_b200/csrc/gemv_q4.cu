@@ -13,9 +13,10 @@
 // cluster, whose sums are joined over distributed shared memory in a fixed order.
 //
 // Measured (B200): 5 rows, 28672 x 7168: 37 us for 116 MB, 0.47 of the copy rate; 16 rows, 50272 x 4096:
-// 41 us for 119 MB; one row, 2048 x 2048: 5.0 us, the launch.  Bound by the half-precision pipe that the
-// dequantizer's multiply-adds and mma.sync share (190 of the 290 cycles that four warps take
-// for a k-block), and by 224 tiles on 148 SMs: two on some, one on others; sharing K out more finely cost
+// 41 us for 119 MB; one row, 2048 x 2048: 5.0 us, the launch (flexq_linear: 64, 62 and 19 us).  The
+// half-precision pipe that the dequantizer's multiply-adds and mma.sync share is busy for 190 of the 290
+// cycles that four warps take for a k-block, which would allow the copy rate; lost are the other
+// 100, a ring that starts empty in every CTA, and 224 tiles on 148 SMs: two on some, one on others.  Sharing K out more finely cost
 // more than it evened out (38 us with two parts, 51 with eight), and so did CTAs of 64 or 32 features
 // (41 and 44 us; 53 and 51 for the larger).  Tried: a warp a K slice with its own ring of
 // 16-byte copies (41 and 50 us: 600 instructions for 2304 bytes, half of them addresses and copies

@@ -14,8 +14,9 @@
 //
 // Memory is the floor of both kernels: rows in, codes and pairs out, and for Q rows in and
 // out.  Measured (B200): 8345 rows of 8 key/value and 32 query heads, d = 128, rotated, to 4 bit:
-// 43 us for 175 MB (rotation and quantization take half the issue slots; prefetched rows, or
-// more or fewer warps an SM, changed nothing; with a check of each code against the reciprocal's
+// 43 us for 175 MB, 0.62 of the copy rate: warps wait for their loads (3.8 of them at each issue, a third
+// of the warps that an SM could hold, 56 % of the issue slots taken); prefetched rows, or
+// more or fewer warps an SM, changed nothing (with a check of each code against the reciprocal's
 // error instead of the corrected quotient 46 us); 2055 rows to fp16, d = 64: 12.5 us for
 // 51 MB; reading 19085 tokens of 32 heads back: 68.5 us for 401 MB, 0.89 of the copy rate (82 us with a
 // lane's two chunks side by side, which its stores then half fill).
