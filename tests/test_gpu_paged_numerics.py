@@ -274,3 +274,32 @@ def test_a_wait_that_runs_out_in_a_piece_is_reported_and_the_next_call_is_right(
     run(outs[1])
     fq.flexq_device_status()
     np.testing.assert_array_equal(to_host(outs[0]).view(np.uint16), to_host(outs[1]).view(np.uint16))
+
+
+@pytest.mark.parametrize("bits,d", [(16, 128), (16, 64)])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_at_the_documented_limit_give_averages_of_values(bits, d, new, sign):
+    """Scores of nearly 2^22, whose last bit is half a power of two of a weight and more: the weights' own
+    size is anyone's, but no weight leaves fp16's range and each result lies among the values (up to the
+    weights' rounding and the output's, 2^-11 each)."""
+    n = 700
+    pg = ph.Paged(bits, 2, 1, d, 16, (new,), (n - new,), seed=d + new)
+    p = np.arange(n)
+    at, sl = pg.table[0, p // 16], p % 16
+    q = np.full((new, 2 * d), 1000.0, np.float16)
+    q[:, 0] = q[:, d] = 64  # one dimension that tells the keys apart: steps of 2 to 3 in the weights' exponent
+    size = 2.0 ** 21.9 * np.sqrt(d) / (1000.0 * (d - 1))
+    pg.k[at, :, sl] = np.float16(sign * size)
+    pg.k[at, :, sl, 0] = (sign * size + np.random.default_rng(0).integers(0, 4, n) * 0.25).astype(np.float16)[:, None]
+    dv = Dev(pg)
+    out = torch.full((new, 2 * d), float("nan"), dtype=torch.float16, device="cuda")
+    fq.flexq_attention_paged(dv.cfg, dv.kv, dv.batch, to_dev(q), 2 * d, out, 2 * d)
+    fq.flexq_device_status()
+    k, v = pg.history(0)
+    s = np.abs(q[0, :d].astype(float) @ k[0, 0]) / np.sqrt(d)
+    assert 2.0 ** 21.5 < s < 2.0 ** 22
+    got = to_host(out).astype(float).reshape(new, 2, d)
+    lo, hi = v[:, 0].min(0), v[:, 0].max(0)
+    slack = 2.0 ** -10 * np.maximum(np.abs(lo), np.abs(hi))
+    assert np.isfinite(got).all() and (got >= lo - slack).all() and (got <= hi + slack).all()
