@@ -639,13 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
       uint64_t sum = 0;        // sums of the even and the odd columns' weights
       int lim = pos - first_of(cur) * kKeys;  // tokens 0 .. lim of the tile count
       __half* dst = a.out + static_cast<size_t>(cur.row0 + tok) * a.ldo + (cur.head * g + c - tok * g) * D;
-      float unit = 0.f;  // of what is put aside in dst: O's columns (D / W) e + u0 .. + 7 at W u0 + 8 e .. + 7
+      float unit = 0.f;   // of what is put aside in dst: O's columns (D / W) e + u0 .. + 7 at W u0 + 8 e .. + 7
+      float aside = 0.f;  // the weights' sum put aside with it
       auto put_aside = [&]() {
         // |O| is at most the weights' sum times 65504 (and 2^-11 of that): with twice the sum's power of two
         // as the unit it is in fp16's range.  Read, add, round, keep the remainder: all exact but the addition.
         float s0, s1;
         unpair(sum, s0, s1);
-        const int ex = (__float_as_int(s0 + s1) >> 23) - 127 + 2;
+        aside += s0 + s1;
+        sum = 0;
+        const int ex = (__float_as_int(aside) >> 23) - 127 + 2;
         const float next = __int_as_float((ex + 127) << 23), inv = __int_as_float((127 - ex) << 23);
 #pragma unroll 1
         for (int x0 = 0; x0 < D; x0 += 32) {  // 16-byte pieces of dst, four at a time
@@ -721,7 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
             const float nb = top > limit ? ceilf(top * a.scale_log2) : base;
             const float alpha = base == -INFINITY ? 0.f : exp2_approx(base - nb);
             base = nb;
-            if (!J && P) unit *= alpha;
+            if (!J && P) {
+              unit *= alpha;
+              aside *= alpha;
+            }
             limit = (nb + kWeightSlack) * inv_scale;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -782,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_chunk_kernel(const Chu
 
         if (!(ok = __all_sync(0xffffffffu, wait(&bar.o_full[m], (o_phase >> m) & 1, DEV_TIMEOUT_EPILOGUE)))) break;
         tc_fence_after();
-        const float inv = 1.f / (s0 + s1);
+        const float inv = 1.f / (s0 + s1 + aside);
 #pragma unroll 1
         for (int u0 = 0; u0 < D / W; u0 += 8) {
           uint32_t o[W][8];

@@ -303,3 +303,31 @@ def test_scores_at_the_documented_limit_give_averages_of_values(bits, d, new, si
     lo, hi = v[:, 0].min(0), v[:, 0].max(0)
     slack = 2.0 ** -10 * np.maximum(np.abs(lo), np.abs(hi))
     assert np.isfinite(got).all() and (got >= lo - slack).all() and (got <= hi + slack).all()
+
+
+@pytest.mark.parametrize("level", [0.03, 0.05, 0.08])
+@pytest.mark.parametrize("n,b,new", [(1600000, 200, 400), (1600000, 1, 20), (1600000, 2, 1), (400000, 4800, 1), (16384, 200, 400)])
+def test_equal_weights_over_long_histories_do_not_drift(level, n, b, new):
+    """Equal weights are the hardest for a running sum: each addition is rounded the same way.  The
+    means over a history's dimensions, in which the outputs' roundings cancel, are off by the weight's
+    one rounding to fp16 (2^-11) and the sums' 2^-12 at the most."""
+    d, page = 64, 1024
+    (k, v, km, vm), _, vd = _positive_pool(4, n, d, page)
+    k.zero_()
+    km.copy_(torch.tensor([level, 0.0], device="cuda").expand_as(km))
+    pages = k.shape[0]
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(b, 1).contiguous()
+    start = torch.arange(0, (b + 1) * new, new, dtype=torch.int32, device="cuda")
+    lens = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    cfg = fq.flexq_config(h=2 * d, heads=2, ffn=8 * d, w_bits=4, kv_bits=4, ln_eps=1e-5)
+    kv = fq.flexq_paged_kv(k.data_ptr(), v.data_ptr(), km.data_ptr(), vm.data_ptr(), 1, pages, page, table.data_ptr(), pages)
+    q = torch.ones(b * new, 2 * d, device="cuda").half()
+    out = torch.full_like(q, float("nan"))
+    fq.flexq_attention_paged(cfg, kv, fq.flexq_ragged(b, b * new, new, n, start.data_ptr(), lens.data_ptr()), q, 2 * d, out,
+                             2 * d)
+    fq.flexq_device_status()
+    for t in {0, new // 2, new - 1}:
+        ref = vd[:n - new + t + 1].mean(0)
+        err = (out[t].double().view(2, d) / ref - 1).cpu().numpy()
+        assert np.abs(err).max() <= 2.0 ** -10 + 2.0 ** -12, np.abs(err).max()
+        assert abs(err.mean()) <= 2.0 ** -11 + 2.0 ** -12, err.mean()
