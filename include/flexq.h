@@ -386,8 +386,8 @@ flexq_status flexq_paged_read(const flexq_config* cfg, const flexq_paged_kv* kv,
  * accumulator memory; a batch that may hold both is two launches.  Scores, the softmax's
  * maximum and sum and the output are held in fp32; the weights enter the
  * product with V in fp16, unnormalised (a weight below 2^-21 of its row's largest to within 2^-31 of
- * that).  The error of the sums over the keys stays below 2^-12, whatever the history's
- * length.  out's rows also hold parts of the result while the call runs.  Cached values below a sequence's
+ * that).  The error of the sums over the keys stays below 2^-12 (single tokens of
+ * histories above 2^22 keys: 2^-11).  out's rows also hold parts of the result while the call runs.  Cached values below a sequence's
  * kv_len must be finite (a later token's weight is zero, but zero times
  * infinity is not), and scores q k / sqrt(d) below 2^22 in magnitude; what slots at and
  * behind kv_len hold does not matter.
